@@ -98,7 +98,8 @@ typedef enum qlin_op {
     QLIN_OP_QUANTIZE_WEIGHT = 3,/* qlin_quantize_weight and qlin_calibrate_input_scale */
     QLIN_OP_INT8_PREP = 4,      /* qlin_int8_prep                                   */
     QLIN_OP_INT8_BLOCK = 5,     /* qlin_int8_block_forward                          */
-    QLIN_OP_FP8_GEMM = 6        /* qlin_fp8_gemm's optional scratch                 */
+    QLIN_OP_FP8_GEMM = 6,       /* qlin_fp8_gemm's optional scratch                 */
+    QLIN_OP_LAYER_NORM_BACKWARD = 7 /* qlin_layer_norm_backward (M, 0, K)           */
 } qlin_op;
 
 /* Bytes of device scratch `op` needs for an [M,K] x [N,K]^T problem (0 when
@@ -268,6 +269,95 @@ QLIN_API qlin_status qlin_fp8_weight_only_forward(const void *X, qlin_dtype xdt,
 QLIN_API qlin_status qlin_int8_block_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K,
                                     const int8_t *Wq, const float *w_scale, int64_t N, const void *bias,
                                     void *Y, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---------------- layer norm in front of a projection ------------------------------ */
+
+/* Layer norm over the K columns of each row:
+ *   mean = sum_k X / K, var = sum_k (X - mean)^2 / K, rstd = 1 / sqrt(var + eps),
+ *   Y = xdt((X - mean) * rstd * gamma + beta), statistics and product in fp32.
+ * gamma, beta [K] in xdt, each nullable (1 and 0: the form whose scale and
+ * shift come from a modulation, or are folded into it). mean, rstd fp32 [M],
+ * each nullable: kept for the backward pass. eps >= 0. Y may be X.
+ * Same shape and alignment rules as the linears (gamma, beta 16-byte aligned;
+ * mean and rstd have no alignment rule here). */
+QLIN_API qlin_status qlin_layer_norm_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *gamma,
+                                    const void *beta, float eps, void *Y, float *mean, float *rstd,
+                                    void *stream);
+
+/* Layer norm written as the FP8 codes that qlin_fp8_gemm takes: the norm and
+ * qlin_fp8_prep in one pass over X, without the 16-bit rounding between them:
+ *   y = (X - mean) * rstd * gamma + beta (fp32), s_x[i] = max_k |y| / 448,
+ *   Xq = e4m3(y * (1 / s_x)); with x_scale (fp32 scalar, device) the static
+ *   form Xq = e4m3(y * (1 / x_scale)) and s_x is not written (may be NULL). */
+QLIN_API qlin_status qlin_layer_norm_fp8_prep(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *gamma,
+                                     const void *beta, float eps, const float *x_scale, uint8_t *Xq,
+                                     float *s_x, void *stream);
+
+/* The same for qlin_w4a8_gemm: per-token int8 codes (round half to even) and
+ * s_x[i] = max_k |y| / 127. */
+QLIN_API qlin_status qlin_layer_norm_w4a8_prep(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *gamma,
+                                      const void *beta, float eps, int8_t *Xq, float *s_x, void *stream);
+
+/* Backward pass of qlin_layer_norm_forward, with xh = (X - mean) * rstd and
+ * d = dY * gamma (fp32):
+ *   dX = xdt(rstd * (d - sum_k d / K - xh * sum_k (d * xh) / K)),
+ *   dgamma = xdt(sum_i dY * xh), dbeta = xdt(sum_i dY), fp32 sums in an order
+ *   that does not depend on timing.
+ * gamma nullable (1). dgamma, dbeta [K], each nullable. M = 0 writes zeros to
+ * them. dX may be dY or X. K <= 16384 (QLIN_ERR_UNSUPPORTED above: a thread
+ * keeps its columns' sums in registers). workspace (needed only for dgamma or
+ * dbeta): qlin_workspace_bytes(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K). */
+QLIN_API qlin_status qlin_layer_norm_backward(const void *dY, const void *X, qlin_dtype xdt, int64_t M, int64_t K,
+                                     const void *gamma, const float *mean, const float *rstd, void *dX,
+                                     void *dgamma, void *dbeta, void *workspace, size_t ws_bytes,
+                                     void *stream);
+
+/* ---------------- low-rank adapters beside a projection ---------------------------- */
+
+/* Bytes of a plan for M rows and L adapters (0 for invalid sizes). Host-only. */
+QLIN_API size_t qlin_lora_plan_bytes(int64_t M, int64_t L);
+
+/* Sorts the rows of a batch by adapter, once for all projections that the
+ * batch passes through. idx int32 [M] (device): the adapter of each row, or
+ * any value outside 0..L-1 for a row without one. plan: device buffer of
+ * qlin_lora_plan_bytes(M, L) bytes, opaque, read by the calls below with the
+ * same M and L (a buffer that holds another M or L leaves their outputs
+ * unwritten, dA and dB zero, and QLIN_ERR_INVALID_ARG in the device status
+ * word). 1 <= L <= 1024, M <= 2^28. */
+QLIN_API qlin_status qlin_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t plan_bytes,
+                           void *stream);
+
+/* Adapters of many requests beside a shared projection, added in place to what
+ * any of the linears wrote:
+ *   H[i] = X[i] A[a]^T (fp32), Y[i] = xdt(Y[i] + scale[a] * H[i] B[a]^T), a = idx[i]
+ * A [L,R,K] and B [L,N,R] in xdt, scale fp32 [L], all R alike (shorter
+ * adapters are padded with zeros). Rows without an adapter keep their Y, bit
+ * for bit. H [M,R] fp32 is written for rows that have one (kept for the
+ * backward pass, else scratch). H enters the second product as two 16-bit
+ * parts (16 significant bits in bf16, 22 in fp16); all sums are fp32 and Y is
+ * rounded once. R % 8 == 0, 8 <= R <= 128; N is arbitrary. A row's result does
+ * not depend on the other rows of the batch beyond the order in which its K
+ * products are added. */
+QLIN_API qlin_status qlin_lora_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A, const void *B,
+                              const float *scale, int64_t L, int64_t R, int64_t N, const void *plan,
+                              size_t plan_bytes, float *H, void *Y, void *stream);
+
+/* Bytes of scratch qlin_lora_backward needs (0 for invalid sizes). Host-only. */
+QLIN_API size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R);
+
+/* Gradients of qlin_lora_forward, dY [M,N] with H as the forward wrote it:
+ *   dH[i] = scale[a] * dY[i] B[a] (fp32)
+ *   dX[i] = xdt(dX[i] + dH[i] A[a])   (in place; rows without an adapter keep
+ *           theirs; dX NULL: not computed)
+ *   dA[a] = xdt(sum_i dH[i]^T X[i]),  dB[a] = xdt(scale[a] * sum_i dY[i]^T H[i])
+ *           over the adapter's rows; zeros for an adapter without rows.
+ * dA and dB are written, not added to, in an order of sums that does not
+ * depend on timing. xdt must be QLIN_BF16 (the parts of dH need fp32's
+ * exponent range); N % 8 == 0. M = 0 writes zeros to dA and dB. */
+QLIN_API qlin_status qlin_lora_backward(const void *dY, const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A,
+                               const void *B, const float *scale, int64_t L, int64_t R, int64_t N,
+                               const void *plan, size_t plan_bytes, const float *H, void *dX, void *dA,
+                               void *dB, void *workspace, size_t ws_bytes, void *stream);
 
 /* ---------------- parity exports: the same kernels, intermediates written out ------ */
 

@@ -30,7 +30,7 @@ QLIN_F16, QLIN_BF16 = 0, 1
 QLIN_W_INT8_ROW, QLIN_W_FP8_TENSOR, QLIN_W_FP8_CHANNEL, QLIN_W_INT4_G128, QLIN_W_INT8_BLOCK32 = 0, 1, 2, 3, 4
 QLIN_W_NVFP4 = 5
 QLIN_OP_INT8_OUTLIER, QLIN_OP_FP8, QLIN_OP_W4A8, QLIN_OP_QUANTIZE_WEIGHT, QLIN_OP_INT8_PREP = 0, 1, 2, 3, 4
-QLIN_OP_INT8_BLOCK, QLIN_OP_FP8_GEMM = 5, 6
+QLIN_OP_INT8_BLOCK, QLIN_OP_FP8_GEMM, QLIN_OP_LAYER_NORM_BACKWARD = 5, 6, 7
 
 _STATUS_NAMES = {0: "QLIN_OK", 1: "QLIN_ERR_INVALID_ARG", 2: "QLIN_ERR_UNSUPPORTED", 3: "QLIN_ERR_ALIGNMENT",
                  4: "QLIN_ERR_WORKSPACE", 5: "QLIN_ERR_CUDA", 6: "QLIN_ERR_TIMEOUT"}
@@ -73,6 +73,15 @@ def _load() -> ctypes.CDLL:
         "qlin_int8_gemm_i32": (st, [P, P, i64, i64, i64, P, P]),
         "qlin_fp8_prep": (st, [P, i32, i64, i64, P, P, P, P]),
         "qlin_e4m3_encode_f32": (st, [P, P, i64, P]),
+        "qlin_layer_norm_forward": (st, [P, i32, i64, i64, P, P, f32, P, P, P, P]),
+        "qlin_layer_norm_fp8_prep": (st, [P, i32, i64, i64, P, P, f32, P, P, P, P]),
+        "qlin_layer_norm_w4a8_prep": (st, [P, i32, i64, i64, P, P, f32, P, P, P]),
+        "qlin_layer_norm_backward": (st, [P, P, i32, i64, i64, P, P, P, P, P, P, P, sz, P]),
+        "qlin_lora_plan_bytes": (sz, [i64, i64]),
+        "qlin_lora_plan": (st, [P, i64, i64, P, sz, P]),
+        "qlin_lora_forward": (st, [P, i32, i64, i64, P, P, P, i64, i64, i64, P, sz, P, P, P]),
+        "qlin_lora_backward_workspace_bytes": (sz, [i64, i64]),
+        "qlin_lora_backward": (st, [P, P, i32, i64, i64, P, P, P, i64, i64, i64, P, sz, P, P, P, P, P, sz, P]),
         "qlin_get_device_status": (st, [P, i32]),
         "qlin_set_wait_timeout_ns": (st, [ctypes.c_uint64]),
         "qlin_set_gemm_schedule": (st, [ctypes.c_int]),
@@ -128,6 +137,28 @@ def _dt(t: torch.Tensor) -> int:
 
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _tensor(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    """Pointer of an argument that the kernel reads or writes at this shape, dtype and device (None: NULL)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, X on {device}")
+    return _ptr(t)
+
+
+def _call(device, fn, *args) -> None:
+    """The C call on the tensors' own device and on that device's current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)))
 
 
 _ws_cache = {}
@@ -459,6 +490,128 @@ def qlin_e4m3_encode_f32(t: torch.Tensor, codes: Optional[torch.Tensor] = None) 
         codes = torch.empty(t.shape, dtype=torch.uint8, device=t.device)
     _check(lib.qlin_e4m3_encode_f32(_ptr(t), _ptr(codes), t.numel(), _stream(t.device)))
     return codes
+
+
+def qlin_layer_norm_forward(X: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                            eps: float = 1e-6, Y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                            rstd: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Layer norm of the rows of X [M,K]. mean, rstd: fp32 [M] to fill for the backward pass. Y may be X."""
+    M, K = X.shape
+    dev = X.device
+    x = _ptr(X)
+    if Y is None:
+        Y = torch.empty_like(X)
+    _call(dev, lib.qlin_layer_norm_forward, x, _dt(X), M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
+          _tensor(beta, "beta", (K,), X.dtype, dev), float(eps), _tensor(Y, "Y", (M, K), X.dtype, dev),
+          _tensor(mean, "mean", (M,), torch.float32, dev), _tensor(rstd, "rstd", (M,), torch.float32, dev))
+    return Y
+
+
+def qlin_layer_norm_fp8_prep(X: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                             eps: float = 1e-6, x_scale: Optional[torch.Tensor] = None):
+    """Layer norm as FP8 codes (uint8 e4m3 [M,K]) and, in dynamic mode, per-token scales [M] for qlin_fp8_gemm."""
+    M, K = X.shape
+    dev = X.device
+    x = _ptr(X)
+    Xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
+    s_x = torch.empty((M,), dtype=torch.float32, device=dev) if x_scale is None else None
+    if x_scale is not None:
+        x_scale = x_scale.reshape(-1)
+    _call(dev, lib.qlin_layer_norm_fp8_prep, x, _dt(X), M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
+          _tensor(beta, "beta", (K,), X.dtype, dev), float(eps), _tensor(x_scale, "x_scale", (1,), torch.float32, dev),
+          _ptr(Xq), _ptr(s_x))
+    return Xq, s_x
+
+
+def qlin_layer_norm_w4a8_prep(X: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                              eps: float = 1e-6):
+    """Layer norm as int8 codes [M,K] and per-token scales [M] for qlin_w4a8_gemm."""
+    M, K = X.shape
+    dev = X.device
+    x = _ptr(X)
+    Xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+    s_x = torch.empty((M,), dtype=torch.float32, device=dev)
+    _call(dev, lib.qlin_layer_norm_w4a8_prep, x, _dt(X), M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
+          _tensor(beta, "beta", (K,), X.dtype, dev), float(eps), _ptr(Xq), _ptr(s_x))
+    return Xq, s_x
+
+
+def qlin_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                             gamma: Optional[torch.Tensor] = None, beta_grad: Optional[bool] = None,
+                             dX: Optional[torch.Tensor] = None):
+    """(dX, dgamma, dbeta) of qlin_layer_norm_forward; dgamma is None without gamma, and dbeta goes with it
+    unless beta_grad says otherwise. dX may be dY or X."""
+    M, K = X.shape
+    dev = X.device
+    x = _ptr(X)
+    if beta_grad is None:
+        beta_grad = gamma is not None
+    if dX is None:
+        dX = torch.empty_like(X)
+    dgamma = torch.empty_like(gamma) if gamma is not None else None
+    dbeta = torch.empty((K,), dtype=X.dtype, device=dev) if beta_grad else None
+    ws = None
+    if dgamma is not None or dbeta is not None:
+        n = int(lib.qlin_workspace_bytes(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K))
+        ws = torch.empty((max(n, 16),), dtype=torch.uint8, device=dev)
+    _call(dev, lib.qlin_layer_norm_backward, _tensor(dY, "dY", (M, K), X.dtype, dev), x, _dt(X), M, K,
+          _tensor(gamma, "gamma", (K,), X.dtype, dev), _tensor(mean, "mean", (M,), torch.float32, dev),
+          _tensor(rstd, "rstd", (M,), torch.float32, dev), _tensor(dX, "dX", (M, K), X.dtype, dev), _ptr(dgamma),
+          _ptr(dbeta), _ptr(ws), 0 if ws is None else ws.numel())
+    return dX, dgamma, dbeta
+
+
+def qlin_lora_plan(idx: torch.Tensor, L: int) -> torch.Tensor:
+    """The rows of a batch sorted by adapter, for the calls below. idx int32 [M]: the adapter of each row, or a
+    value outside 0..L-1 for a row without one. Made once per batch, used by every projection it passes through."""
+    if idx.dim() != 1 or idx.dtype != torch.int32:
+        raise TypeError("idx must be a 1-D int32 tensor")
+    M, L = idx.shape[0], int(L)
+    x = _ptr(idx)
+    n = int(lib.qlin_lora_plan_bytes(M, L))
+    plan = torch.empty((max(n, 16),), dtype=torch.uint8, device=idx.device)
+    _call(idx.device, lib.qlin_lora_plan, x, M, L, _ptr(plan), plan.numel())
+    return plan
+
+
+def _lora_args(X, A, B, scale, plan):
+    M, K = X.shape
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [L, R, K] and B [L, N, R]")
+    L, R, N = A.shape[0], A.shape[1], B.shape[1]
+    dev = X.device
+    if plan.numel() != max(int(lib.qlin_lora_plan_bytes(M, L)), 16):
+        raise ValueError(f"plan was not made for {M} rows and {L} adapters")
+    return M, K, L, R, N, dev, (_tensor(A, "A", (L, R, K), X.dtype, dev), _tensor(B, "B", (L, N, R), X.dtype, dev),
+                                _tensor(scale, "scale", (L,), torch.float32, dev), L, R, N,
+                                _tensor(plan, "plan", plan.shape, torch.uint8, dev), plan.numel())
+
+
+def qlin_lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, plan: torch.Tensor,
+                      Y: torch.Tensor, H: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Adapters beside a projection, in place: Y[i] += scale[a] * (X[i] A[a]^T) B[a]^T for rows with an adapter.
+    H: fp32 [M,R] to fill with X A^T for the backward pass (rows without an adapter are left as they were)."""
+    x = _ptr(X)
+    M, K, L, R, N, dev, args = _lora_args(X, A, B, scale, plan)
+    if H is None:
+        H = torch.empty((M, R), dtype=torch.float32, device=dev)
+    _call(dev, lib.qlin_lora_forward, x, _dt(X), M, K, *args, _tensor(H, "H", (M, R), torch.float32, dev),
+          _tensor(Y, "Y", (M, N), X.dtype, dev))
+    return Y
+
+
+def qlin_lora_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                       plan: torch.Tensor, H: torch.Tensor, dX: Optional[torch.Tensor] = None):
+    """(dX, dA, dB) of qlin_lora_forward, bf16. dX: the projection's own input gradient, added to in place
+    (None: not computed)."""
+    x = _ptr(X)
+    M, K, L, R, N, dev, args = _lora_args(X, A, B, scale, plan)
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    ws = torch.empty((max(int(lib.qlin_lora_backward_workspace_bytes(M, R)), 16),), dtype=torch.uint8, device=dev)
+    _call(dev, lib.qlin_lora_backward, _tensor(dY, "dY", (M, N), X.dtype, dev), x, _dt(X), M, K, *args,
+          _tensor(H, "H", (M, R), torch.float32, dev), _tensor(dX, "dX", (M, K), X.dtype, dev), _ptr(dA), _ptr(dB),
+          _ptr(ws), ws.numel())
+    return dX, dA, dB
 
 
 def qlin_get_device_status(reset: bool = False) -> int:

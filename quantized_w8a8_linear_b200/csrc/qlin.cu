@@ -21,6 +21,8 @@
 #include "gemm.cuh"
 #include "gemm_w4a8.cuh"
 #include "gemm_cvt.cuh"
+#include "lora.cuh"
+#include "norm.cuh"
 #include "prep.cuh"
 
 using namespace qlin;
@@ -547,6 +549,10 @@ qlin_status int8_outlier_gemm_ws(qlin_dtype xdt, int64_t M, int64_t K, const int
   return launch_gemm<0, EPI_INT8_OUTLIER, __half>(w.Xq, Wq, ep, st, 2, w.sk_ctas);
 }
 
+// CTAs of k_norm_bwd at most: each leaves 2 K fp32 column sums for the second
+// kernel, so wide rows take two CTAs per SM and short ones as many as fit.
+int64_t norm_bwd_ctas(int64_t K) { return std::min<int64_t>(std::max<int64_t>((int64_t{1} << 20) / K, 296), 4736); }
+
 #define QLIN_TRY(...)                  \
   do {                                 \
     qlin_status _s = (__VA_ARGS__);    \
@@ -588,6 +594,8 @@ size_t qlin_workspace_bytes(qlin_op op, int64_t M, int64_t N, int64_t K) {
       return 256;
     case QLIN_OP_INT8_BLOCK:
       return static_cast<size_t>(round_up(2 * M * K, 256) + round_up(4 * M, 256));
+    case QLIN_OP_LAYER_NORM_BACKWARD:
+      return static_cast<size_t>(8 * K * std::min<int64_t>(M, norm_bwd_ctas(K)));
     default:
       return 0;
   }
@@ -1349,3 +1357,430 @@ extern "C" qlin_status qlin_int8_outlier_forward_noalloc(const void* X, qlin_dty
 
 
 
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+namespace {
+
+// Dynamic shared memory above 48 KB has to be allowed once per kernel and device.
+template <typename Kern>
+qlin_status allow_smem(Kern kern, int bytes, std::atomic<bool> (&set)[16]) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 16 || set[dev].load(std::memory_order_acquire)) return QLIN_OK;
+  const qlin_status s = check_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), "cudaFuncSetAttribute");
+  if (s == QLIN_OK) set[dev].store(true, std::memory_order_release);
+  return s;
+}
+
+// A launch as a programmatic dependent of the kernel before it, in clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+qlin_status launch_dependent(void (*kern)(P...), const char* what, int64_t grid, int threads, int smem, int cluster, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return check_cuda(cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...), what);
+}
+
+template <typename T, int V, int OUT>
+qlin_status launch_norm_fwd_v(const NormArgs& a, int threads, int sms, cudaStream_t st) {
+  auto kern = k_norm_fwd<T, V, OUT>;
+  const int smem = NORM_STAGES * V * threads * 16;
+  static std::atomic<bool> set[16] = {};
+  qlin_status s = allow_smem(kern, NORM_STAGES * V * NORM_MAX_THREADS * 16, set);
+  if (s != QLIN_OK) return s;
+  int per_sm = 0;
+  s = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem), "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  if (s != QLIN_OK) return s;
+  if (per_sm < 1) return fail(QLIN_ERR_UNSUPPORTED, "layer norm does not fit on an SM");
+  const int64_t grid = std::min<int64_t>(a.M, static_cast<int64_t>(per_sm) * sms);
+  kern<<<static_cast<unsigned>(grid), threads, smem, st>>>(a);
+  return check_cuda(cudaGetLastError(), "k_norm_fwd launch");
+}
+
+template <typename T, int OUT>
+qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
+  DeviceInfo* d;
+  qlin_status s = device_info(&d);
+  if (s != QLIN_OK) return s;
+  const int64_t KV = a.K / 8;
+  // two vectors of a row per thread while there are rows for every SM to
+  // overlap, one when a row's latency counts (and 16 warps a row at most)
+  const int64_t want = a.M >= 4 * d->sms ? 2 : 1;
+  const int64_t warps = std::min<int64_t>(std::max<int64_t>((KV + 32 * want - 1) / (32 * want), 1), NORM_MAX_THREADS / 32);
+  const int64_t per = (KV + 32 * warps - 1) / (32 * warps);
+  const int threads = static_cast<int>(32 * warps);
+  if (per <= 1) return launch_norm_fwd_v<T, 1, OUT>(a, threads, d->sms, st);
+  if (per <= 2) return launch_norm_fwd_v<T, 2, OUT>(a, threads, d->sms, st);
+  if (per <= 4) return launch_norm_fwd_v<T, 4, OUT>(a, threads, d->sms, st);
+  return launch_norm_fwd_v<T, 8, OUT>(a, threads, d->sms, st);
+}
+
+template <typename T, int V, bool COLS>
+qlin_status launch_norm_bwd_v(const NormBwdArgs& a, int threads, int sms, int64_t& ctas, cudaStream_t st) {
+  auto kern = k_norm_bwd<T, V, COLS>;
+  const int smem = NORM_STAGES * 2 * V * threads * 16;
+  static std::atomic<bool> set[16] = {};
+  qlin_status s = allow_smem(kern, NORM_STAGES * 2 * V * NORM_MAX_THREADS * 16, set);
+  if (s != QLIN_OK) return s;
+  int per_sm = 0;
+  s = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem), "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  if (s != QLIN_OK) return s;
+  if (per_sm < 1) return fail(QLIN_ERR_UNSUPPORTED, "layer norm's backward pass does not fit on an SM");
+  ctas = std::min<int64_t>(std::min<int64_t>(a.M, static_cast<int64_t>(per_sm) * sms), norm_bwd_ctas(a.K));
+  kern<<<static_cast<unsigned>(ctas), threads, smem, st>>>(a);
+  return check_cuda(cudaGetLastError(), "k_norm_bwd launch");
+}
+
+template <typename T>
+qlin_status norm_bwd(const NormBwdArgs& a, void* dgamma, void* dbeta, cudaStream_t st) {
+  DeviceInfo* d;
+  qlin_status s = device_info(&d);
+  if (s != QLIN_OK) return s;
+  const int64_t KV = a.K / 8;
+  const int64_t V = std::max<int64_t>((KV + NORM_MAX_THREADS - 1) / NORM_MAX_THREADS, 1);
+  const int threads = static_cast<int>((KV + 32 * V - 1) / (32 * V) * 32);
+  int64_t ctas = 0;
+#define QLIN_NORM_BWD(v)                                                          \
+  s = a.part != nullptr ? launch_norm_bwd_v<T, v, true>(a, threads, d->sms, ctas, st) \
+                        : launch_norm_bwd_v<T, v, false>(a, threads, d->sms, ctas, st)
+  if (V == 1) QLIN_NORM_BWD(1);
+  else if (V == 2) QLIN_NORM_BWD(2);
+  else if (V == 3) QLIN_NORM_BWD(3);
+  else QLIN_NORM_BWD(4);
+#undef QLIN_NORM_BWD
+  if (s != QLIN_OK || a.part == nullptr) return s;
+  return launch_dependent(k_norm_bwd_cols<T>, "k_norm_bwd_cols launch", 2 * a.K / 32, 512, 0, 1, st, static_cast<const float*>(a.part), a.K,
+                          static_cast<int>(ctas), static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
+}
+
+qlin_status check_norm(const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* gamma, const void* beta, float eps) {
+  QLIN_TRY(check_common(X, xdt, M, K, 0));
+  if (!(eps >= 0.0f) || std::isinf(eps)) return fail(QLIN_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!aligned16(gamma)) return fail(QLIN_ERR_ALIGNMENT, "gamma is not 16-byte aligned");
+  if (!aligned16(beta)) return fail(QLIN_ERR_ALIGNMENT, "beta is not 16-byte aligned");
+  return QLIN_OK;
+}
+
+NormArgs norm_args(const void* X, int64_t M, int64_t K, const void* gamma, const void* beta, float eps, void* Y) {
+  NormArgs a{};
+  a.M = M; a.K = K; a.eps = eps; a.Y = Y;
+  a.X = static_cast<const uint16_t*>(X);
+  a.gamma = static_cast<const uint16_t*>(gamma);
+  a.beta = static_cast<const uint16_t*>(beta);
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+qlin_status qlin_layer_norm_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* gamma, const void* beta, float eps,
+                                    void* Y, float* mean, float* rstd, void* stream) {
+  QLIN_TRY(check_norm(X, xdt, M, K, gamma, beta, eps));
+  if (M == 0) return ok();
+  QLIN_REQ_PTR(Y, "Y");
+  NormArgs a = norm_args(X, M, K, gamma, beta, eps, Y);
+  a.mean = mean;
+  a.rstd = rstd;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  QLIN_TRY(xdt == QLIN_BF16 ? launch_norm_fwd<__nv_bfloat16, NORM_OUT_16>(a, st) : launch_norm_fwd<__half, NORM_OUT_16>(a, st));
+  return ok();
+}
+
+qlin_status qlin_layer_norm_fp8_prep(const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* gamma, const void* beta, float eps,
+                                     const float* x_scale, uint8_t* Xq, float* s_x, void* stream) {
+  QLIN_TRY(check_norm(X, xdt, M, K, gamma, beta, eps));
+  if (M == 0) return ok();
+  QLIN_REQ_PTR(Xq, "Xq");
+  if (x_scale == nullptr) QLIN_REQ_PTR(s_x, "s_x");
+  NormArgs a = norm_args(X, M, K, gamma, beta, eps, Xq);
+  a.s_x = s_x;
+  a.x_scale = x_scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = xdt == QLIN_BF16;
+  if (x_scale != nullptr)
+    QLIN_TRY(bf ? launch_norm_fwd<__nv_bfloat16, NORM_OUT_E4M3_STATIC>(a, st) : launch_norm_fwd<__half, NORM_OUT_E4M3_STATIC>(a, st));
+  else
+    QLIN_TRY(bf ? launch_norm_fwd<__nv_bfloat16, NORM_OUT_E4M3>(a, st) : launch_norm_fwd<__half, NORM_OUT_E4M3>(a, st));
+  return ok();
+}
+
+qlin_status qlin_layer_norm_w4a8_prep(const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* gamma, const void* beta, float eps,
+                                      int8_t* Xq, float* s_x, void* stream) {
+  QLIN_TRY(check_norm(X, xdt, M, K, gamma, beta, eps));
+  if (M == 0) return ok();
+  QLIN_REQ_PTR(Xq, "Xq");
+  QLIN_REQ_PTR(s_x, "s_x");
+  NormArgs a = norm_args(X, M, K, gamma, beta, eps, Xq);
+  a.s_x = s_x;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  QLIN_TRY(xdt == QLIN_BF16 ? launch_norm_fwd<__nv_bfloat16, NORM_OUT_INT8>(a, st) : launch_norm_fwd<__half, NORM_OUT_INT8>(a, st));
+  return ok();
+}
+
+qlin_status qlin_layer_norm_backward(const void* dY, const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* gamma, const float* mean,
+                                     const float* rstd, void* dX, void* dgamma, void* dbeta, void* workspace, size_t ws_bytes, void* stream) {
+  QLIN_TRY(check_norm(X, xdt, M, K, gamma, nullptr, 0.0f));
+  if (K > 16384) return fail(QLIN_ERR_UNSUPPORTED, "layer norm's backward pass takes K up to 16384 (got %lld)", static_cast<long long>(K));
+  if (!aligned16(dgamma)) return fail(QLIN_ERR_ALIGNMENT, "dgamma is not 16-byte aligned");
+  if (!aligned16(dbeta)) return fail(QLIN_ERR_ALIGNMENT, "dbeta is not 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool cols = dgamma != nullptr || dbeta != nullptr;
+  if (M == 0) {   // sums over no rows
+    if (dgamma != nullptr) QLIN_TRY(check_cuda(cudaMemsetAsync(dgamma, 0, static_cast<size_t>(2 * K), st), "cudaMemsetAsync"));
+    if (dbeta != nullptr) QLIN_TRY(check_cuda(cudaMemsetAsync(dbeta, 0, static_cast<size_t>(2 * K), st), "cudaMemsetAsync"));
+    return ok();
+  }
+  QLIN_REQ_PTR(dY, "dY");
+  QLIN_REQ_PTR(mean, "mean");
+  QLIN_REQ_PTR(rstd, "rstd");
+  QLIN_REQ_PTR(dX, "dX");
+  if (cols) {
+    if (workspace == nullptr || ws_bytes < qlin_workspace_bytes(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K))
+      return fail(QLIN_ERR_WORKSPACE, "workspace too small (need %zu bytes)", qlin_workspace_bytes(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K));
+    QLIN_REQ_PTR(workspace, "workspace");
+  }
+  NormBwdArgs a{};
+  a.M = M; a.K = K;
+  a.dY = static_cast<const uint16_t*>(dY);
+  a.X = static_cast<const uint16_t*>(X);
+  a.gamma = static_cast<const uint16_t*>(gamma);
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dX = static_cast<uint16_t*>(dX);
+  a.part = cols ? static_cast<float*>(workspace) : nullptr;
+  QLIN_TRY(xdt == QLIN_BF16 ? norm_bwd<__nv_bfloat16>(a, dgamma, dbeta, st) : norm_bwd<__half>(a, dgamma, dbeta, st));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// low-rank adapters
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kLoraMaxM = int64_t{1} << 28;
+constexpr int LORA_WG_MAX_CTAS = 160;
+
+// 16-bit row-major [rows, cols] for row gathers of 64 columns (box one row high), 128B swizzle.
+qlin_status make_tmap_gather(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  QLIN_TRY(get_encode(&enc));
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * 2)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(LORA_BK), 1u};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QLIN_ERR_CUDA, "cuTensorMapEncodeTiled (gather) failed (%d)", static_cast<int>(r));
+  return QLIN_OK;
+}
+
+// Adapter weights 16-bit [L, rows, cols]: box 64 columns x box_rows of one
+// adapter, 128B swizzle; rows past `rows` read as zeros, not as the next adapter's.
+qlin_status make_tmap_adapters(CUtensorMap* m, const void* base, int64_t L, int64_t rows, int64_t cols, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  QLIN_TRY(get_encode(&enc));
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(L)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * 2), static_cast<cuuint64_t>(rows * cols * 2)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(LORA_BK), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QLIN_ERR_CUDA, "cuTensorMapEncodeTiled (adapters) failed (%d)", static_cast<int>(r));
+  return QLIN_OK;
+}
+
+struct LoraCall {
+  int64_t M, L, R;
+  const int* plan;
+  const float* scale;
+  DeviceInfo* d;
+  cudaStream_t st;
+  LoraPlan view() const { return LoraPlan{plan, M, L}; }
+};
+
+// H [M,R] = scale * X W^T; X [M,C]. W_MN: W is B [L,C,R], else A [L,R,C].
+template <typename T, int RB, bool W_MN>
+qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H) {
+  CUtensorMap tx, tw;
+  QLIN_TRY(make_tmap_gather(&tx, X, c.M, C));
+  if (W_MN) QLIN_TRY(make_tmap_adapters(&tw, W, c.L, C, c.R, LORA_BK));
+  else QLIN_TRY(make_tmap_adapters(&tw, W, c.L, c.R, C, static_cast<int>(round_up(c.R, 16))));
+  auto kern = k_lora_shrink<T, RB, W_MN>;
+  constexpr int smem = LoraShrinkSmem<RB>::TOTAL;
+  static std::atomic<bool> set[16] = {};
+  QLIN_TRY(allow_smem(kern, smem, set));
+  // the largest cluster whose CTAs are resident together (two per SM) when the
+  // tiles are full, and that leaves every CTA a block of the contraction
+  const int64_t full = (c.M + LORA_TILE - 1) / LORA_TILE;
+  int cluster = 8;
+  while (cluster > 1 && (full * cluster > 2 * c.d->sms || cluster > (C + LORA_BK - 1) / LORA_BK)) cluster /= 2;
+  LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), scale, H};
+  return launch_dependent(kern, "k_lora_shrink launch", lora_max_tiles(c.M, c.L) * cluster, LORA_SHRINK_THREADS, smem, cluster, c.st, tx, tw, p, cluster);
+}
+template <typename T, bool W_MN>
+qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H) {
+  return c.R <= 64 ? launch_lora_shrink_rb<T, 1, W_MN>(c, X, C, W, scale, H) : launch_lora_shrink_rb<T, 2, W_MN>(c, X, C, W, scale, H);
+}
+
+// Y [M,N] += scale * H V^T. V_MN: V is A [L,R,N], else B [L,N,R].
+template <typename T, int RB, bool V_MN, bool VEC>
+qlin_status launch_lora_expand_rb(const LoraCall& c, const float* H, const void* V, int64_t N, const float* scale, void* Y) {
+  CUtensorMap tv, ty;
+  if (V_MN) QLIN_TRY(make_tmap_adapters(&tv, V, c.L, c.R, N, static_cast<int>(round_up(c.R, 16))));
+  else QLIN_TRY(make_tmap_adapters(&tv, V, c.L, N, c.R, LORA_EXPAND_BN));
+  std::memset(&ty, 0, sizeof(ty));
+  if (VEC) QLIN_TRY(make_tmap_gather(&ty, Y, c.M, N));
+  auto kern = k_lora_expand<T, RB, V_MN, VEC>;
+  constexpr int smem = LoraExpandSmem<RB, VEC>::TOTAL;
+  static_assert(smem <= 227 * 1024, "k_lora_expand shared memory");
+  static std::atomic<bool> set[16] = {};
+  QLIN_TRY(allow_smem(kern, smem, set));
+  const int64_t most = lora_max_tiles(c.M, c.L) * ((N + LORA_EXPAND_BN - 1) / LORA_EXPAND_BN);
+  const int64_t grid = std::min<int64_t>(most, (smem <= 113 * 1024 ? 2 : 1) * c.d->sms);
+  LoraExpandParams p{c.view(), N, static_cast<int>(c.R), scale, H, static_cast<uint16_t*>(Y)};
+  return launch_dependent(kern, "k_lora_expand launch", grid, LORA_EXPAND_THREADS, smem, 1, c.st, tv, ty, p);
+}
+template <typename T, bool V_MN>
+qlin_status launch_lora_expand(const LoraCall& c, const float* H, const void* V, int64_t N, const float* scale, void* Y) {
+  if (N % 8 == 0)
+    return c.R <= 64 ? launch_lora_expand_rb<T, 1, V_MN, true>(c, H, V, N, scale, Y) : launch_lora_expand_rb<T, 2, V_MN, true>(c, H, V, N, scale, Y);
+  if constexpr (V_MN) return fail(QLIN_ERR_ALIGNMENT, "K must be a multiple of 8");
+  else return c.R <= 64 ? launch_lora_expand_rb<T, 1, V_MN, false>(c, H, V, N, scale, Y) : launch_lora_expand_rb<T, 2, V_MN, false>(c, H, V, N, scale, Y);
+}
+
+int lora_wg_ctas(const DeviceInfo* d) { return std::min(d->sms, LORA_WG_MAX_CTAS); }
+
+template <int RB>
+qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const float* dH, void* dA, const void* dY, int64_t N, const float* H,
+                              void* dB, float* part) {
+  CUtensorMap t0, t1;
+  QLIN_TRY(make_tmap_gather(&t0, X, c.M, K));
+  QLIN_TRY(make_tmap_gather(&t1, dY, c.M, N));
+  auto kern = k_lora_wgrad<RB>;
+  constexpr int smem = LoraWgradSmem<RB>::TOTAL;
+  static std::atomic<bool> set[16] = {};
+  QLIN_TRY(allow_smem(kern, smem, set));
+  LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {dH, H}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
+  QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", p.ctas, LORA_WG_THREADS, smem, 1, c.st, t0, t1, p));
+  const int64_t items = ((K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS) * c.L * (c.R / 8);
+  return launch_dependent(k_lora_wgrad_join, "k_lora_wgrad_join launch", std::min<int64_t>(items, 8 * c.d->sms), LORA_WG_COLS, 0, 1, c.st, p);
+}
+
+qlin_status check_lora(int64_t M, int64_t L, int64_t R, const void* A, const void* B, const float* scale, const void* plan, size_t plan_bytes) {
+  if (L < 1 || L > LORA_MAX_L) return fail(QLIN_ERR_UNSUPPORTED, "L must be 1..%d adapters (got %lld)", LORA_MAX_L, static_cast<long long>(L));
+  if (M > kLoraMaxM) return fail(QLIN_ERR_UNSUPPORTED, "M = %lld exceeds %lld", static_cast<long long>(M), static_cast<long long>(kLoraMaxM));
+  if (R <= 0 || R % 8 != 0) return fail(QLIN_ERR_ALIGNMENT, "R must be a positive multiple of 8 (got %lld)", static_cast<long long>(R));
+  if (R > LORA_MAX_R) return fail(QLIN_ERR_UNSUPPORTED, "R = %lld exceeds %d", static_cast<long long>(R), LORA_MAX_R);
+  QLIN_REQ_PTR(A, "A");
+  QLIN_REQ_PTR(B, "B");
+  QLIN_REQ_PTR(scale, "scale");
+  QLIN_REQ_PTR(plan, "plan");
+  if (plan_bytes < qlin_lora_plan_bytes(M, L))
+    return fail(QLIN_ERR_WORKSPACE, "plan has %zu bytes, a plan of M = %lld, L = %lld has %zu", plan_bytes, static_cast<long long>(M),
+                static_cast<long long>(L), qlin_lora_plan_bytes(M, L));
+  return QLIN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlin_lora_plan_bytes(int64_t M, int64_t L) {
+  if (M < 0 || M > kLoraMaxM || L < 1 || L > LORA_MAX_L) return 0;
+  return static_cast<size_t>(4 * lora_plan_words(M, L));
+}
+
+qlin_status qlin_lora_plan(const int32_t* idx, int64_t M, int64_t L, void* plan, size_t plan_bytes, void* stream) {
+  if (M < 0) return fail(QLIN_ERR_INVALID_ARG, "negative size");
+  if (L < 1 || L > LORA_MAX_L) return fail(QLIN_ERR_UNSUPPORTED, "L must be 1..%d adapters (got %lld)", LORA_MAX_L, static_cast<long long>(L));
+  if (M > kLoraMaxM) return fail(QLIN_ERR_UNSUPPORTED, "M = %lld exceeds %lld", static_cast<long long>(M), static_cast<long long>(kLoraMaxM));
+  if (M > 0) QLIN_REQ_PTR(idx, "idx");
+  QLIN_REQ_PTR(plan, "plan");
+  if (plan_bytes < qlin_lora_plan_bytes(M, L))
+    return fail(QLIN_ERR_WORKSPACE, "plan too small (need %zu bytes)", qlin_lora_plan_bytes(M, L));
+  DeviceInfo* d;
+  QLIN_TRY(device_info(&d));
+  static std::atomic<bool> set[16] = {};
+  QLIN_TRY(allow_smem(k_lora_plan, 32 * LORA_MAX_L * 4, set));
+  k_lora_plan<<<1, LORA_PLAN_THREADS, static_cast<size_t>(32 * L * 4), static_cast<cudaStream_t>(stream)>>>(idx, M, L, static_cast<int*>(plan));
+  QLIN_TRY(check_cuda(cudaGetLastError(), "k_lora_plan launch"));
+  return ok();
+}
+
+qlin_status qlin_lora_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* A, const void* B, const float* scale, int64_t L,
+                              int64_t R, int64_t N, const void* plan, size_t plan_bytes, float* H, void* Y, void* stream) {
+  QLIN_TRY(check_common(X, xdt, M, K, N));
+  if (M == 0 || N == 0) return ok();
+  QLIN_TRY(check_lora(M, L, R, A, B, scale, plan, plan_bytes));
+  QLIN_REQ_PTR(H, "H");
+  QLIN_REQ_PTR(Y, "Y");
+  DeviceInfo* d;
+  QLIN_TRY(device_info(&d));
+  const LoraCall c{M, L, R, static_cast<const int*>(plan), scale, d, static_cast<cudaStream_t>(stream)};
+  if (xdt == QLIN_BF16) {
+    QLIN_TRY((launch_lora_shrink<__nv_bfloat16, false>(c, X, K, A, nullptr, H)));
+    QLIN_TRY((launch_lora_expand<__nv_bfloat16, false>(c, H, B, N, scale, Y)));
+  } else {
+    QLIN_TRY((launch_lora_shrink<__half, false>(c, X, K, A, nullptr, H)));
+    QLIN_TRY((launch_lora_expand<__half, false>(c, H, B, N, scale, Y)));
+  }
+  return ok();
+}
+
+size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R) {
+  if (M < 0 || R <= 0) return 0;
+  return static_cast<size_t>(round_up(4 * M * R, 256) + 4 * R * 2 * LORA_WG_COLS * LORA_WG_MAX_CTAS);
+}
+
+qlin_status qlin_lora_backward(const void* dY, const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* A, const void* B,
+                               const float* scale, int64_t L, int64_t R, int64_t N, const void* plan, size_t plan_bytes, const float* H,
+                               void* dX, void* dA, void* dB, void* workspace, size_t ws_bytes, void* stream) {
+  QLIN_TRY(check_common(X, xdt, M, K, N));
+  if (xdt != QLIN_BF16) return fail(QLIN_ERR_UNSUPPORTED, "the adapters' backward pass is bf16 only");
+  if (N == 0 || N % 8 != 0) return fail(QLIN_ERR_ALIGNMENT, "N must be a positive multiple of 8 (got %lld)", static_cast<long long>(N));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (L < 1 || L > LORA_MAX_L) return fail(QLIN_ERR_UNSUPPORTED, "L must be 1..%d adapters (got %lld)", LORA_MAX_L, static_cast<long long>(L));
+  if (R <= 0 || R % 8 != 0) return fail(QLIN_ERR_ALIGNMENT, "R must be a positive multiple of 8 (got %lld)", static_cast<long long>(R));
+  QLIN_REQ_PTR(dA, "dA");
+  QLIN_REQ_PTR(dB, "dB");
+  if (M == 0) {   // sums over no rows
+    QLIN_TRY(check_cuda(cudaMemsetAsync(dA, 0, static_cast<size_t>(2 * L * R * K), st), "cudaMemsetAsync"));
+    QLIN_TRY(check_cuda(cudaMemsetAsync(dB, 0, static_cast<size_t>(2 * L * R * N), st), "cudaMemsetAsync"));
+    return ok();
+  }
+  QLIN_TRY(check_lora(M, L, R, A, B, scale, plan, plan_bytes));
+  QLIN_REQ_PTR(dY, "dY");
+  QLIN_REQ_PTR(H, "H");
+  if (dX != nullptr && !aligned16(dX)) return fail(QLIN_ERR_ALIGNMENT, "dX is not 16-byte aligned");
+  if (workspace == nullptr || ws_bytes < qlin_lora_backward_workspace_bytes(M, R))
+    return fail(QLIN_ERR_WORKSPACE, "workspace too small (need %zu bytes)", qlin_lora_backward_workspace_bytes(M, R));
+  QLIN_REQ_PTR(workspace, "workspace");
+  DeviceInfo* d;
+  QLIN_TRY(device_info(&d));
+  const LoraCall c{M, L, R, static_cast<const int*>(plan), scale, d, st};
+  float* dH = static_cast<float*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round_up(4 * M * R, 256));
+  using T = __nv_bfloat16;
+  QLIN_TRY((launch_lora_shrink<T, true>(c, dY, N, B, scale, dH)));
+  QLIN_TRY(R <= 64 ? launch_lora_wgrad<1>(c, X, K, dH, dA, dY, N, H, dB, part) : launch_lora_wgrad<2>(c, X, K, dH, dA, dY, N, H, dB, part));
+  if (dX != nullptr) QLIN_TRY((launch_lora_expand<T, true>(c, dH, A, K, nullptr, dX)));
+  return ok();
+}
+
+}  // extern "C"
