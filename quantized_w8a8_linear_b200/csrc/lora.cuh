@@ -10,10 +10,12 @@
 // A plan sorts the rows by adapter once per batch (k_lora_plan): tiles of up
 // to 128 rows of one adapter, as lists of row numbers. Every kernel works on
 // tiles, so each row meets its own adapter only, whatever the order of the
-// rows, and gathers them with TMA (tile::gather4: four rows of 128 bytes an
-// instruction; a row number past the tensor reads as zeros). The products are
-// thin (R <= 128), so all three kernels are bound by the 16-bit matrices they
-// read and write, not by the tensor cores:
+// rows, and gathers them with 16-byte cp.async copies into the swizzled
+// layout the tensor core reads (TMA row gathers, tile::gather4, moved 512
+// bytes in about 60 cycles per SM: 54 us against 21 us of HBM time for the
+// first product of 16640 x 4096 rows). The products are thin (R <= 128), so
+// all three kernels are bound by the 16-bit matrices they read and write, not
+// by the tensor cores:
 //   k_lora_shrink  H or dH: contraction over K or N;
 //   k_lora_expand  Y or dX: contraction over R;
 //   k_lora_wgrad   dA and dB: contraction over the rows of an adapter.
@@ -146,12 +148,20 @@ __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx,
 // ---------------------------------------------------------------------------
 // helpers
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, const int4& r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-      : "memory");
+// 16-byte asynchronous global -> shared copy, or 16 zero bytes.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(copy ? 16 : 0) : "memory");
+}
+
+// Arrives on `bar` once all cp.async copies this thread issued so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// ... or the first `bytes` of them (none, where bytes <= 0) and zeros.
+__device__ __forceinline__ void cp_async_upto16(uint32_t dst, const void* src, int64_t bytes) {
+  const int n = bytes >= 16 ? 16 : bytes > 0 ? static_cast<int>(bytes) : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
@@ -244,21 +254,24 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo
 // of all of them in rank order (distributed shared memory; no workspace and
 // no second kernel). c is chosen so that few tiles still fill the SMs.
 // ---------------------------------------------------------------------------
-constexpr int LORA_SHRINK_THREADS = 192;   // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr int LORA_SHRINK_THREADS = 160;   // warps 0-3 copies, then the epilogue; warp 4 MMA
+constexpr int LORA_SHRINK_BK = 128;        // contraction of a stage: 256 bytes of a row
 
 struct LoraShrinkParams {
   LoraPlan plan;
   int64_t C;            // contraction length (K, or N)
   int R;
+  const uint16_t* X;    // [M,C]
   const float* scale;   // [L], or nullptr: 1
   float* H;             // [M,R]
 };
 
 template <int RB>   // ceil(R / 64)
 struct LoraShrinkSmem {
-  static constexpr int STAGES = 4;
-  static constexpr int A_BYTES = LORA_TILE * 128;
-  static constexpr int W_BYTES = RB * 64 * 128;
+  static constexpr int STAGES = RB == 1 ? 2 : 3;   // two CTAs an SM, or one
+  static constexpr int AHEAD = STAGES - 1;          // stages a thread's copies run ahead of the one it hands over
+  static constexpr int A_BYTES = 2 * LORA_TILE * 128;   // two halves of 64 columns
+  static constexpr int W_BYTES = 2 * RB * 64 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2) + 16;
   static constexpr int TOTAL = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
@@ -268,8 +281,7 @@ struct LoraShrinkSmem {
 
 template <typename T, int RB, bool W_MN>
 __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
-    k_lora_shrink(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const LoraShrinkParams p,
-                  const int cluster) {
+    k_lora_shrink(const __grid_constant__ CUtensorMap tmW, const LoraShrinkParams p, const int cluster) {
   using S = LoraShrinkSmem<RB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -286,17 +298,16 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(&full_bar[s], 1);
+      mbar_init(&full_bar[s], 5);   // four copying warps, and the copy of W
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(tfull_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
-    tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
-  if (warp == 1) {
+  if (warp == 4) {
     tmem_alloc(tmem_slot, TCOLS);
     tmem_relinquish();
   }
@@ -313,89 +324,109 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
   const bool work = tile < p.plan.tiles();   // the same in all CTAs of the cluster
   const int2 info = work ? p.plan.info(tile) : make_int2(0, 0);
   const int a = info.x, n = info.y;
-  const int kbs = static_cast<int>((p.C + LORA_BK - 1) / LORA_BK);
+  const int kbs = static_cast<int>((p.C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK);
   const int kb0 = static_cast<int>(static_cast<int64_t>(kbs) * rank / cluster);
   const int kb1 = static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / cluster);
   const int Rp = (p.R + 15) / 16 * 16;
 
-  if (work && warp == 0) {
-    // ---------------- TMA producer: lane i gathers rows 4 i .. 4 i + 3 ----------------
-    const int groups = (n + 3) / 4;
-    const int4 r4 = reinterpret_cast<const int4*>(p.plan.rows(tile))[lane];
-    const uint32_t bytes = static_cast<uint32_t>(groups * 512 + (W_MN ? RB * 64 : Rp) * 128);
-    int stage = 0;
+  if (work && warp < 4) {
+    // ---------------- copies: chunk c of rows r0, r0 + 8, ..., 16 lanes a row ----------------
+    const int c = lane & 15, r0 = threadIdx.x >> 4;
+    const int* rows = p.plan.rows(tile);
+    int src[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) src[i] = r0 + 8 * i < n ? rows[r0 + 8 * i] : -1;
+    const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128 + (((c & 7) ^ r0) << 4));
+    int stage = 0, ready = 0;
     uint32_t phase = 0, issued = 0;
     bool good = true;
+    auto hand_over = [&]() {   // the oldest stage not handed over: this thread's copies of it have landed
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_bar[ready]);
+      if (++ready == S::STAGES) ready = 0;
+    };
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (lane == 0) {
-        good = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
-        if (good) mbar_arrive_expect_tx(&full_bar[stage], bytes);
-      }
-      good = __shfl_sync(0xffffffffu, good, 0);
+      good = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
       if (!good) break;
-      if (lane < groups) tma_gather4(sA(stage) + lane * 512, &tmX, &full_bar[stage], kb * LORA_BK, r4);
-      if (lane == 0) {
+      if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(&full_bar[stage], static_cast<uint32_t>(W_MN ? S::W_BYTES : 2 * Rp * 128));
         if constexpr (W_MN) {
 #pragma unroll
-          for (int b = 0; b < RB; ++b) tma_load_3d(sW(stage) + b * 8192, &tmW, &full_bar[stage], b * 64, kb * LORA_BK, a);
+          for (int b = 0; b < RB; ++b) tma_load_3d(sW(stage) + b * 16384, &tmW, &full_bar[stage], b * 64, kb * LORA_SHRINK_BK, a);
         } else {
-          tma_load_3d(sW(stage), &tmW, &full_bar[stage], kb * LORA_BK, 0, a);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tma_load_3d(sW(stage) + h * RB * 8192, &tmW, &full_bar[stage], kb * LORA_SHRINK_BK + h * 64, 0, a);
         }
       }
+      const uint32_t d = smem_u32(sA(stage)) + off;
+      const bool in = kb * LORA_SHRINK_BK + 8 * c < p.C;
+      const uint16_t* x = p.X + (in ? kb * LORA_SHRINK_BK + 8 * c : 0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (src[i] >= 0) cp_async16_or_zero(d + 1024u * i, x + src[i] * p.C, in);
+      cp_async_commit();
       issued |= 1u << stage;
+      if (kb - kb0 >= S::AHEAD) {
+        cp_async_wait<S::AHEAD>();
+        hand_over();
+      }
       if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
     }
-    if (!good && lane == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
-  } else if (work && warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-      const uint32_t idesc = W_MN ? (idesc_f16(LORA_TILE, RB * 64, bf) | IDESC_B_MN) : idesc_f16(LORA_TILE, Rp, bf);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full_bar[stage], phase, abort_flag)) break;
-        tc_fence_after();
-        const uint64_t adesc = sdesc_k128(smem_u32(sA(stage)));
-        const uint64_t bdesc = W_MN ? sdesc_mn128(smem_u32(sW(stage)), 8192u) : sdesc_k128(smem_u32(sW(stage)));
-#pragma unroll
-        for (int k = 0; k < LORA_BK / 16; ++k)
-          umma<2>(tmem_base, adesc + 2u * k, bdesc + (W_MN ? 128u : 2u) * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
-        umma_commit(&empty_bar[stage]);
-        if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
-      }
-      umma_commit(tfull_bar);
-      drain_mma(drain_bar);
+    cp_async_wait<0>();
+    if (good) {
+      for (int i = kb1 - kb0 < S::AHEAD ? kb1 - kb0 : S::AHEAD; i > 0; --i) hand_over();
+    } else if (threadIdx.x == 0) {
+      drain_ring(full_bar, S::STAGES, stage, phase, issued);
     }
-  } else if (work) {
     // ---------------- epilogue: row q * 32 + lane of the tile ----------------
-    const int q = warp & 3;
+    const int q = warp;
     const int r = q * 32 + lane;
-    const bool good = mbar_wait(tfull_bar, 0, abort_flag) && kb1 > kb0;
+    good = __all_sync(0xffffffffu, good && mbar_wait(tfull_bar, 0, abort_flag)) && kb1 > kb0;
     tc_fence_after();
     const float s = p.scale != nullptr ? __ldg(p.scale + a) : 1.0f;
-    float* out = cluster > 1 ? reinterpret_cast<float*>(smem) + r * (Rp + 4)
-                             : p.H + static_cast<int64_t>(r < n ? p.plan.rows(tile)[r] : 0) * p.R;
+    float* out = cluster > 1 ? reinterpret_cast<float*>(smem) + r * (Rp + 4) : p.H + static_cast<int64_t>(r < n ? rows[r] : 0) * p.R;
     if (q * 32 < n) {
-      for (int c = 0; c < p.R; c += 16) {
+      for (int c0 = 0; c0 < p.R; c0 += 16) {
         uint32_t v[16];
         __syncwarp();
-        tmem_ld16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c, v);
+        tmem_ld16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
         tmem_wait16(v);
         if (r < n) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            if (c + i < p.R) {
+            if (c0 + i < p.R) {
               float4 f = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
               if (!good) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               if (cluster == 1) f = make_float4(f.x * s, f.y * s, f.z * s, f.w * s);
-              *reinterpret_cast<float4*>(out + c + i) = f;
+              *reinterpret_cast<float4*>(out + c0 + i) = f;
             }
           }
         }
       }
     }
     tc_fence_before();
+  } else if (work && lane == 0) {
+    // ---------------- MMA issuer ----------------
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    const uint32_t idesc = W_MN ? (idesc_f16(LORA_TILE, RB * 64, bf) | IDESC_B_MN) : idesc_f16(LORA_TILE, Rp, bf);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(&full_bar[stage], phase, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t as = smem_u32(sA(stage)), ws = smem_u32(sW(stage));
+#pragma unroll
+      for (int k = 0; k < LORA_SHRINK_BK / 16; ++k) {
+        const uint64_t adesc = sdesc_k128(as + (k >> 2) * (LORA_TILE * 128)) + 2u * (k & 3);
+        const uint64_t bdesc = W_MN ? sdesc_mn128(ws, 16384u) + 128u * k : sdesc_k128(ws + (k >> 2) * (RB * 8192)) + 2u * (k & 3);
+        umma<2>(tmem_base, adesc, bdesc, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+      }
+      umma_commit(&empty_bar[stage]);
+      if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+    }
+    umma_commit(tfull_bar);
+    drain_mma(drain_bar);
   }
   if (cluster > 1) {
     cluster_sync();
@@ -418,7 +449,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     cluster_sync();   // no CTA leaves while another reads its partial tile
   }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 4) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, TCOLS);
@@ -426,21 +457,29 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
 }
 
 // ---------------------------------------------------------------------------
-// k_lora_expand: Y[rows of the tile] += s (hi + lo) V^T, 64 columns a unit.
+// k_lora_expand: Y[rows of the tile] += s (hi + lo) V^T, 128 columns a unit.
 //   V_MN 0: V = B[a] [N, R], K-major;   1: V = A[a] [R, K] read as its
 //   transpose, MN-major, with Y = dX and K columns.
-// Persistent: the units (tile, 64 columns), columns fastest, are cut into one
-// equal range per CTA, so that every SM moves the same number of bytes
-// whatever the tiles; a range spans few tiles, whose H is split into its
-// parts once each. Y comes in through TMA gathers beside V, is updated in
-// place in shared memory and leaves in 128-byte row pieces. The copies of Y
-// and V start before the kernel that makes H has ended (programmatic
-// dependent launch); only the readers of H wait for it.
-//   VEC false: rows of Y that are not multiples of 16 bytes are read and
-//   written two bytes at a time by the epilogue instead.
+// Persistent, one CTA an SM: the units (tile, 128 columns), columns fastest,
+// are cut into one equal range per CTA, so that every SM moves the same number
+// of bytes whatever the tiles; a range spans few tiles, whose H is split into
+// its parts once each. Y comes in by cp.async, up to three units ahead, into
+// rows of 272 bytes (a row a thread and a row a few lanes are both free of
+// bank conflicts), is updated there by the thread that holds the row's
+// accumulator, and leaves in 128-byte pieces of rows; two groups of eight
+// warps take turns at the units, since one group's chain of waits, loads and
+// stores took longer than a unit's bytes. 256 bytes of a row at a
+// time are what HBM wants: reading and writing 128 rows of 24 KB in place,
+// walked in pieces of 64, 128, 256 and 512 bytes, runs at 4.2, 4.6, 5.2 and
+// 5.3 TB/s. The copies of Y and V start before the kernel that makes H has
+// ended (programmatic dependent launch); only the readers of H wait for it.
+//   VEC false: rows of Y that are not multiples of 16 bytes. A row's piece
+// then lies `shift` bytes into its 17 aligned 16-byte chunks, in shared memory
+// as in global memory, so that the copies in stay whole chunks; on the way out
+// the two chunks that a piece shares with its neighbours go element by element.
 // ---------------------------------------------------------------------------
-constexpr int LORA_EXPAND_THREADS = 192;   // warp 0 TMA, warp 1 MMA, warps 2-5 split H and the epilogue
-constexpr int LORA_EXPAND_BN = 64;
+constexpr int LORA_EXPAND_THREADS = 704;   // warps 0-3 copy Y, warp 4 copies V, warp 5 MMA, warps 6-21 split H and the epilogue
+constexpr int LORA_EXPAND_BN = 128;
 
 struct LoraExpandParams {
   LoraPlan plan;
@@ -451,56 +490,62 @@ struct LoraExpandParams {
   uint16_t* Y;          // [M,N]
 };
 
-template <int RB, bool VEC>
+template <int RB>
 struct LoraExpandSmem {
-  static constexpr int STAGES = 3;
+  static constexpr int V_STAGES = 2;
+  static constexpr int Y_STAGES = RB == 1 ? 4 : 2;
   static constexpr int H_BYTES = RB * LORA_TILE * 128;                 // one part
-  static constexpr int V_BYTES = RB * 64 * 128;
-  static constexpr int Y_BYTES = VEC ? LORA_TILE * 128 : 0;
-  static constexpr int STAGE_BYTES = V_BYTES + Y_BYTES;
-  static constexpr int D_BYTES = VEC ? 0 : LORA_TILE * 65 * 4;         // update staged for the 2-byte path
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 6) + 16;
-  static constexpr int TOTAL = 1024 + 2 * H_BYTES + STAGES * STAGE_BYTES + D_BYTES + BAR_BYTES;
+  static constexpr int V_BYTES = RB * LORA_EXPAND_BN * 128;
+  static constexpr int Y_ROW = 272;
+  static constexpr int Y_BYTES = LORA_TILE * Y_ROW;
+  static constexpr int BAR_BYTES = 8 * (2 * V_STAGES + 2 * Y_STAGES + 7) + 16;
+  static constexpr int TOTAL = 1024 + 2 * H_BYTES + V_STAGES * V_BYTES + Y_STAGES * Y_BYTES + BAR_BYTES;
+  static_assert(TOTAL <= 227 * 1024, "k_lora_expand shared memory");
 };
 
 template <typename T, int RB, bool V_MN, bool VEC>
-__global__ void __launch_bounds__(LORA_EXPAND_THREADS)
-    k_lora_expand(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmY, const LoraExpandParams p) {
-  using S = LoraExpandSmem<RB, VEC>;
+__global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __grid_constant__ CUtensorMap tmV, const LoraExpandParams p) {
+  using S = LoraExpandSmem<RB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sH = smem;   // [hi, lo][RB][128 rows][128 bytes]
-  auto sV = [&](int s) { return smem + 2 * S::H_BYTES + s * S::STAGE_BYTES; };
-  auto sY = [&](int s) { return smem + 2 * S::H_BYTES + s * S::STAGE_BYTES + S::V_BYTES; };
-  float* sD = reinterpret_cast<float*>(smem + 2 * S::H_BYTES + S::STAGES * S::STAGE_BYTES);
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + 2 * S::H_BYTES + S::STAGES * S::STAGE_BYTES + S::D_BYTES);
-  uint64_t* empty_bar = full_bar + S::STAGES;
-  uint64_t* tfull_bar = empty_bar + S::STAGES;   // [2]
-  uint64_t* tempty_bar = tfull_bar + 2;          // [2]
+  auto sV = [&](int s) { return smem + 2 * S::H_BYTES + s * S::V_BYTES; };
+  auto sY = [&](int s) { return smem + 2 * S::H_BYTES + S::V_STAGES * S::V_BYTES + s * S::Y_BYTES; };
+  uint64_t* vfull_bar = reinterpret_cast<uint64_t*>(smem + 2 * S::H_BYTES + S::V_STAGES * S::V_BYTES + S::Y_STAGES * S::Y_BYTES);
+  uint64_t* vempty_bar = vfull_bar + S::V_STAGES;
+  uint64_t* yfull_bar = vempty_bar + S::V_STAGES;
+  uint64_t* yempty_bar = yfull_bar + S::Y_STAGES;
+  uint64_t* tfull_bar = yempty_bar + S::Y_STAGES;   // [2]
+  uint64_t* tempty_bar = tfull_bar + 2;             // [2]
   uint64_t* hfull_bar = tempty_bar + 2;
-  uint64_t* drain_bar = hfull_bar + 1;
+  uint64_t* hempty_bar = hfull_bar + 1;
+  uint64_t* drain_bar = hempty_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t TCOLS = 2 * LORA_EXPAND_BN;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 4);
+    for (int s = 0; s < S::V_STAGES; ++s) {
+      mbar_init(&vfull_bar[s], 1);
+      mbar_init(&vempty_bar[s], 1);
+    }
+    for (int s = 0; s < S::Y_STAGES; ++s) {
+      mbar_init(&yfull_bar[s], 128);
+      mbar_init(&yempty_bar[s], 8);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], 4);
+      mbar_init(&tempty_bar[b], 8);
     }
-    mbar_init(hfull_bar, 4);
+    mbar_init(hfull_bar, 16);
+    mbar_init(hempty_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmV);
-    if (VEC) tma_prefetch_desc(&tmY);
   }
-  if (warp == 1) {
+  if (warp == 5) {
     tmem_alloc(tmem_slot, TCOLS);
     tmem_relinquish();
   }
@@ -512,98 +557,146 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS)
   const int nbs = static_cast<int>((p.N + LORA_EXPAND_BN - 1) / LORA_EXPAND_BN);
   const int64_t units = static_cast<int64_t>(p.plan.tiles()) * nbs;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int t0 = static_cast<int>(u0 / nbs), nb0 = static_cast<int>(u0 % nbs);   // first tile and columns
   const int Rp = (p.R + 15) / 16 * 16;
+  // byte of its aligned 16-byte chunk at which the piece of `row` from column n0 starts
+  auto shift_of = [&](int64_t row, int64_t n0) { return VEC ? 0 : static_cast<int>((2 * (row * p.N + n0)) & 15); };
 
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    int stage = 0, tile = -1, a = 0, groups = 0;
-    int4 r4 = make_int4(0, 0, 0, 0);
-    uint32_t phase = 0, issued = 0;
-    bool good = true;
-    for (int64_t u = u0; u < u1; ++u) {
-      const int t = static_cast<int>(u / nbs), n0 = static_cast<int>(u % nbs) * LORA_EXPAND_BN;
-      if (t != tile) {
-        tile = t;
-        const int2 info = p.plan.info(t);
-        a = info.x;
-        groups = (info.y + 3) / 4;
-        r4 = reinterpret_cast<const int4*>(p.plan.rows(t))[lane];
-      }
-      if (lane == 0) {
-        good = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
-        if (good) mbar_arrive_expect_tx(&full_bar[stage], static_cast<uint32_t>((V_MN ? Rp * 128 : RB * 8192) + (VEC ? groups * 512 : 0)));
-      }
-      good = __shfl_sync(0xffffffffu, good, 0);
-      if (!good) break;
-      if (VEC && lane < groups) tma_gather4(sY(stage) + lane * 512, &tmY, &full_bar[stage], n0, r4);
-      if (lane == 0) {
-        if constexpr (V_MN) {
-          tma_load_3d(sV(stage), &tmV, &full_bar[stage], n0, 0, a);
-        } else {
+  if (warp < 4) {
+    // ---------------- copies of Y: chunk c of rows r0, r0 + 8, ..., 16 lanes a row ----------------
+    const int c = lane & 15, r0 = threadIdx.x >> 4;
+    const int64_t all = 2 * p.plan.M * p.N;   // bytes of Y
+    const uint8_t* Y = reinterpret_cast<const uint8_t*>(p.Y);
+    int rows[16];
+    int stage = 0, n = 0;
+    uint32_t phase = 0;
+    bool good = true, next = true;
+    for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
+      if (next) {
+        n = p.plan.info(static_cast<int>(t)).y;
 #pragma unroll
-          for (int b = 0; b < RB; ++b) tma_load_3d(sV(stage) + b * 8192, &tmV, &full_bar[stage], b * 64, n0, a);
+        for (int i = 0; i < 16; ++i) rows[i] = r0 + 8 * i < n ? p.plan.rows(static_cast<int>(t))[r0 + 8 * i] : -1;
+      }
+      good = __all_sync(0xffffffffu, mbar_wait(&yempty_bar[stage], phase ^ 1u, abort_flag));
+      if (!good) break;
+      const int64_t n0 = nb * LORA_EXPAND_BN;
+      const int bytes = static_cast<int>(2 * (p.N - n0 < LORA_EXPAND_BN ? p.N - n0 : LORA_EXPAND_BN));
+      const uint32_t d = smem_u32(sY(stage)) + r0 * S::Y_ROW;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (rows[i] >= 0) {
+          const int64_t b = 2 * (rows[i] * p.N + n0);
+          const int shift = VEC ? 0 : static_cast<int>(b & 15);
+          const int64_t at = b - shift + 16 * c;
+          if (16 * c < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i + 16 * c, Y + at, VEC ? 16 : all - at);
+          if (!VEC && c == 0 && 256 < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i + 256, Y + at + 256, all - at - 256);
         }
       }
-      issued |= 1u << stage;
-      if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+      cp_async_arrive(&yfull_bar[stage]);
+      if (++stage == S::Y_STAGES) { stage = 0; phase ^= 1u; }
+      next = ++nb == nbs;
+      if (next) {
+        nb = 0;
+        ++t;
+      }
     }
-    if (!good && lane == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
-  } else if (warp == 1) {
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == 4) {
+    if (lane == 0) {
+      // ---------------- TMA producer: V ----------------
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool good = true;
+      int a = u0 < u1 ? p.plan.info(t0).x : 0;
+      for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
+        const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
+        good = mbar_wait(&vempty_bar[stage], phase ^ 1u, abort_flag);
+        if (!good) break;
+        mbar_arrive_expect_tx(&vfull_bar[stage], static_cast<uint32_t>(V_MN ? 2 * Rp * 128 : S::V_BYTES));
+        if constexpr (V_MN) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tma_load_3d(sV(stage) + h * Rp * 128, &tmV, &vfull_bar[stage], n0 + 64 * h, 0, a);
+        } else {
+#pragma unroll
+          for (int b = 0; b < RB; ++b) tma_load_3d(sV(stage) + b * (LORA_EXPAND_BN * 128), &tmV, &vfull_bar[stage], b * 64, n0, a);
+        }
+        issued |= 1u << stage;
+        if (++stage == S::V_STAGES) { stage = 0; phase ^= 1u; }
+        if (++nb == nbs) {
+          nb = 0;
+          if (u + 1 < u1) a = p.plan.info(static_cast<int>(++t)).x;
+        }
+      }
+      if (!good) drain_ring(vfull_bar, S::V_STAGES, stage, phase, issued);
+    }
+  } else if (warp == 5) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16(LORA_TILE, LORA_EXPAND_BN, std::is_same<T, __nv_bfloat16>::value) | (V_MN ? IDESC_B_MN : 0u);
       const int ksteps = Rp / 16;
-      int stage = 0, acc = 0, tile = -1;
+      int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, h_phase = 0;
-      for (int64_t u = u0; u < u1; ++u) {
-        const int t = static_cast<int>(u / nbs);
-        if (t != tile) {
-          tile = t;
+      bool next = true;
+      for (int64_t u = u0, nb = nb0; u < u1; ++u) {
+        if (next) {
           if (!mbar_wait(hfull_bar, h_phase, abort_flag)) break;
           h_phase ^= 1u;
         }
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag)) break;
-        if (!mbar_wait(&full_bar[stage], phase, abort_flag)) break;
+        if (!mbar_wait(&vfull_bar[stage], phase, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * LORA_EXPAND_BN);
         const uint32_t v = smem_u32(sV(stage)), h = smem_u32(sH);
         for (int part = 0; part < 2; ++part) {
           for (int k = 0; k < ksteps; ++k) {
             const uint64_t adesc = sdesc_k128(h + part * S::H_BYTES + (k >> 2) * (LORA_TILE * 128)) + 2u * (k & 3);
-            const uint64_t bdesc = V_MN ? sdesc_mn128(v, 0u) + 128u * k : sdesc_k128(v + (k >> 2) * 8192) + 2u * (k & 3);
+            const uint64_t bdesc = V_MN ? sdesc_mn128(v, static_cast<uint32_t>(Rp * 128)) + 128u * k : sdesc_k128(v + (k >> 2) * (LORA_EXPAND_BN * 128)) + 2u * (k & 3);
             umma<2>(d, adesc, bdesc, idesc, (part | k) != 0 ? 1u : 0u);
           }
         }
+        umma_commit(&vempty_bar[stage]);
         umma_commit(&tfull_bar[acc]);
-        if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+        if (++stage == S::V_STAGES) { stage = 0; phase ^= 1u; }
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        next = ++nb == nbs;
+        if (next) {
+          nb = 0;
+          umma_commit(hempty_bar);
+        }
       }
       drain_mma(drain_bar);
     }
   } else {
-    // ---------------- H's parts, then the epilogue: warp for rows 32 q .. 32 q + 31 ----------------
-    const int q = warp & 3;
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    int stage = 0, acc = 0, tile = -1, n = 0, my_row = 0;
+    // ---------------- H's parts, then the epilogue: rows 32 q .. 32 q + 31, columns 64 half .. 64 half + 63 ----------------
+    const int q = warp & 3, half = (warp - 6) >> 2 & 1, group = warp >= 14;   // group: of the units it takes, and of their accumulators
+    const uint32_t tmem = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(group * LORA_EXPAND_BN + 64 * half);
+    int stage = 0, n = 0, my_row = 0;
     float s = 1.0f;    // scale[a], times the power of two of the lane's row (fp16)
-    uint32_t phase = 0, acc_phase = 0;
-    bool good = true;
-    griddep_wait();    // H
-    for (int64_t u = u0; u < u1; ++u) {
-      const int t = static_cast<int>(u / nbs);
-      const int64_t n0 = (u % nbs) * LORA_EXPAND_BN;
-      if (t != tile) {
-        // the MMAs that read the previous tile's parts have completed: this
-        // warp has waited for the accumulator of its last unit
-        tile = t;
-        const int2 info = p.plan.info(t);
+    uint32_t phase = 0, acc_phase = 0, h_phase = 0;
+    bool next = true, good = true;
+    for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
+      if (next) {
+        const int2 info = p.plan.info(static_cast<int>(t));
         n = info.y - q * 32;
-        my_row = n > lane ? p.plan.rows(t)[q * 32 + lane] : 0;
+        my_row = n > lane ? p.plan.rows(static_cast<int>(t))[q * 32 + lane] : 0;
+        if (u == u0) {
+          griddep_wait();    // H
+        } else {             // the MMAs that read the previous tile's parts
+          good = __all_sync(0xffffffffu, mbar_wait(hempty_bar, h_phase, abort_flag));
+          if (!good) break;
+          h_phase ^= 1u;
+        }
         const float sa = p.scale != nullptr ? __ldg(p.scale + info.x) : 1.0f;
         s = sa;
+        constexpr bool F16 = std::is_same<T, __half>::value;
         constexpr int CH = RB * 8;   // 8-value chunks of a row: lanes of a warp that share a row
+        // the four warps of these rows take every fourth step of 32 / CH rows; in
+        // fp16 all look at all of them, for their lanes' powers of two
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
+          const bool mine = (i & 3) == 2 * group + half;
+          if (!F16 && !mine) continue;
           const int e = i * 32 + lane, r = e / CH, c = e % CH;
           float f[8] = {};
           const int row = __shfl_sync(0xffffffffu, my_row, r);
@@ -613,7 +706,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS)
             f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
             f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
           }
-          if constexpr (std::is_same<T, __half>::value) {
+          if constexpr (F16) {
             float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
@@ -630,81 +723,114 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS)
             const float up_mine = __shfl_sync(0xffffffffu, up, (lane % (32 / CH)) * CH);
             if (lane / (32 / CH) == i) s = sa * up_mine;
           }
-          uint4 hi, lo;
-          split8<T>(f, hi, lo);
-          const int rr = q * 32 + r;
-          uint8_t* d = sH + (c >> 3) * (LORA_TILE * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-          *reinterpret_cast<uint4*>(d) = hi;
-          *reinterpret_cast<uint4*>(d + S::H_BYTES) = lo;
+          if (mine) {
+            uint4 hi, lo;
+            split8<T>(f, hi, lo);
+            const int rr = q * 32 + r;
+            uint8_t* h = sH + (c >> 3) * (LORA_TILE * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+            *reinterpret_cast<uint4*>(h) = hi;
+            *reinterpret_cast<uint4*>(h + S::H_BYTES) = lo;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(hfull_bar);
       }
-      if (VEC) good = mbar_wait(&full_bar[stage], phase, abort_flag);   // Y, written by TMA
-      good = good && mbar_wait(&tfull_bar[acc], acc_phase, abort_flag);
-      if (!__all_sync(0xffffffffu, good)) break;
+      if (((u - u0) & 1) == group) {
+      good = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[group], acc_phase, abort_flag) && mbar_wait(&yfull_bar[stage], phase, abort_flag));
+      if (!good) break;
+      acc_phase ^= 1u;
       tc_fence_after();
       if (n > 0) {
-        uint32_t v[2][32];
-        tmem_ld32(lane_base + static_cast<uint32_t>(acc * LORA_EXPAND_BN), v[0]);
-        tmem_ld32(lane_base + static_cast<uint32_t>(acc * LORA_EXPAND_BN + 32), v[1]);
-        tmem_wait_regs32(v[0]);
-        tmem_wait_regs32(v[1]);
-        tc_fence_before();
-        if constexpr (VEC) {
-          const int rr = q * 32 + lane;
-          uint8_t* yr = sY(stage) + rr * 128;
+        const int64_t n0 = nb * LORA_EXPAND_BN;
+        uint8_t* yr = sY(stage) + q * 32 * S::Y_ROW;   // the warp's rows
+        const int shift = shift_of(my_row, n0);
+        uint8_t* mine = yr + lane * S::Y_ROW + 128 * half + (VEC ? 0 : shift & ~3);
+        const uint32_t odd = VEC ? 0 : (shift & 2) * 8;   // 16: pairs of columns straddle 32-bit words
+        uint32_t before = 0;                              // VEC false: the previous pair
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(yr + ((c ^ (rr & 7)) << 4));
-            float f[8];
-            uint16_t h[8];
-            unpack8(*at, h);
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem + static_cast<uint32_t>(c), v);
+          tmem_wait16(v);
+          auto sum_of = [&](int j) { return __uint_as_float(v[j]); };
+          if constexpr (VEC) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = fmaf(__uint_as_float(v[c >> 2][(c & 3) * 8 + i]), s, to_f<T>(h[i]));
-            *at = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-          }
-          __syncwarp();
-          const int c = lane & 7;
+            for (int h = 0; h < 2; ++h) {
+              uint4* at = reinterpret_cast<uint4*>(mine + 2 * c + 16 * h);
+              float f[8];
+              widen8<T>(*at, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3), row = __shfl_sync(0xffffffffu, my_row, r);
-            if (r < n && n0 + 8 * c < p.N)
-              *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(row) * p.N + n0 + 8 * c) =
-                  *reinterpret_cast<const uint4*>(sY(stage) + (q * 32 + r) * 128 + ((c ^ (r & 7)) << 4));
-          }
-        } else {
-          float* d = sD + (q * 32) * 65;
+              for (int i = 0; i < 8; ++i) f[i] = fmaf(sum_of(8 * h + i), s, f[i]);
+              *at = narrow8<T>(f);
+            }
+          } else {
+            uint32_t* w = reinterpret_cast<uint32_t*>(mine + 2 * c);
 #pragma unroll
-          for (int i = 0; i < 64; ++i) d[lane * 65 + i] = __uint_as_float(v[i >> 5][i & 31]) * s;
-          __syncwarp();
-          const int rows = n < 32 ? n : 32;
-#pragma unroll 4
-          for (int r = 0; r < rows; ++r) {
-            uint16_t* y = p.Y + static_cast<int64_t>(__shfl_sync(0xffffffffu, my_row, r)) * p.N + n0;
-#pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-              if (n0 + h + lane < p.N) y[h + lane] = from_f<T>(to_f<T>(y[h + lane]) + d[r * 65 + h + lane]);
+            for (int i = 0; i < 8; ++i) {
+              // words not yet written: w[i + 1], and the upper half of w[i] (its lower half is the previous pair's)
+              const uint32_t pair = __funnelshift_r(w[i], odd ? w[i + 1] : 0u, odd);
+              const uint32_t sum = narrow2<T>(fmaf(sum_of(2 * i), s, to_f<T>(static_cast<uint16_t>(pair))),
+                                            fmaf(sum_of(2 * i + 1), s, to_f<T>(static_cast<uint16_t>(pair >> 16))));
+              if (odd && c + i == 0) reinterpret_cast<uint16_t*>(w)[1] = static_cast<uint16_t>(sum);   // the lower half is another warp's
+              else w[i] = __funnelshift_l(before, sum, odd);
+              before = sum;
+              if (odd) {
+                // keep the second half of the pair where the next one, or another warp, leaves it alone
+                if (c + 2 * i == 62) reinterpret_cast<uint16_t*>(w)[2 * (i + 1)] = static_cast<uint16_t>(sum >> 16);
+              }
             }
           }
-          __syncwarp();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty_bar[group]);   // the accumulator is in shared memory
+        // out: eight lanes a row, 16-byte chunk c of the warp's 128 bytes of it
+        const int c = lane & 7;
+        const int64_t col = n0 + 64 * half;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          const int64_t row = __shfl_sync(0xffffffffu, my_row, r);
+          if (r < n) {
+            const uint8_t* src = yr + r * S::Y_ROW + 128 * half;
+            uint8_t* dst = reinterpret_cast<uint8_t*>(p.Y + row * p.N + col);
+            if constexpr (VEC) {
+              if (col + 8 * c < p.N) *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(src + 16 * c);
+            } else {
+              const int sh = shift_of(row, n0);
+              const int cols = p.N - col < 64 ? static_cast<int>(p.N - col) : 64;
+              // elements [e0, e0 + 8) of the warp's 64 lie in one chunk; with a shift, the last lane has the first and last pieces
+              const int e0 = sh == 0 ? 8 * c : 8 * c + (16 - sh) / 2;
+              if (e0 + 8 <= 64 && e0 + 8 <= cols) {
+                *reinterpret_cast<uint4*>(dst + 2 * e0) = *reinterpret_cast<const uint4*>(src + sh + 2 * e0);
+              } else {
+                for (int e = e0; e < 64 && e < cols; ++e)
+                  *reinterpret_cast<uint16_t*>(dst + 2 * e) = *reinterpret_cast<const uint16_t*>(src + sh + 2 * e);
+              }
+              if (sh != 0 && c == 7)
+                for (int e = 0; e < (16 - sh) / 2 && e < cols; ++e)
+                  *reinterpret_cast<uint16_t*>(dst + 2 * e) = *reinterpret_cast<const uint16_t*>(src + sh + 2 * e);
+            }
+          }
+        }
+      } else if (lane == 0) {
+        mbar_arrive(&tempty_bar[group]);
       }
-      // this warp's generic accesses to the stage come before the next copy into it
-      if (VEC) fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&tempty_bar[acc]);
-        mbar_arrive(&empty_bar[stage]);
+      if (lane == 0) mbar_arrive(&yempty_bar[stage]);
       }
-      if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      if (++stage == S::Y_STAGES) { stage = 0; phase ^= 1u; }
+      next = ++nb == nbs;
+      if (next) {
+        nb = 0;
+        ++t;
+      }
     }
   }
   __syncthreads();
   griddep_wait();
-  if (warp == 1) {
+  if (warp == 5) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, TCOLS);
@@ -726,7 +852,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS)
 // bf16 only: G's parts need fp32's exponent range (a power of two per row, as
 // k_lora_expand takes out, does not leave a sum over rows).
 // ---------------------------------------------------------------------------
-constexpr int LORA_WG_THREADS = 448;   // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue, warps 6-13 split G
+constexpr int LORA_WG_THREADS = 544;   // warps 0-3 copies, warp 4 MMA, warps 5-8 epilogue, warps 9-16 split G
 constexpr int LORA_WG_CONV_WARPS = 8;
 constexpr int LORA_WG_COLS = 256;      // columns of a unit: two MMAs of M = 128
 
@@ -734,6 +860,7 @@ struct LoraWgradParams {
   LoraPlan plan;
   int R, ctas;
   int64_t cols[2];       // K, N
+  const uint16_t* X[2];  // X [M,K], dY [M,N]
   const float* G[2];     // dH, H [M,R]
   const float* scale;    // [L]
   uint16_t* out[2];      // dA [L,R,K], dB [L,N,R]
@@ -759,6 +886,7 @@ struct LoraWgradUnits {
 template <int RB>
 struct LoraWgradSmem {
   static constexpr int STAGES = RB == 1 ? 4 : 3;
+  static constexpr int AHEAD = STAGES - 2;
   static constexpr int X_BYTES = 2 * LORA_TILE * 128;            // 128 columns of the tile: two 64-column halves
   static constexpr int G_BYTES = RB * LORA_TILE * 128;           // one part
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 9) + 16;
@@ -767,8 +895,7 @@ struct LoraWgradSmem {
 };
 
 template <int RB>
-__global__ void __launch_bounds__(LORA_WG_THREADS, 1)
-    k_lora_wgrad(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const LoraWgradParams p) {
+__global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgradParams p) {
   using T = __nv_bfloat16;
   using S = LoraWgradSmem<RB>;
   extern __shared__ uint8_t smem_raw[];
@@ -790,7 +917,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(&full_bar[s], 1);
+      mbar_init(&full_bar[s], 4);
       mbar_init(&empty_bar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -802,10 +929,8 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
-    tma_prefetch_desc(&tm0);
-    tma_prefetch_desc(&tm1);
   }
-  if (warp == 1) {
+  if (warp == 4) {
     tmem_alloc(tmem_slot, TCOLS);
     tmem_relinquish();
   }
@@ -819,35 +944,75 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
   const LoraWgradUnits un(p);
   const int64_t u0 = un.first(blockIdx.x), u1 = un.first(blockIdx.x + 1);
 
-  if (warp == 0) {
-    // ---------------- TMA producer: 128 columns of the tile a stage ----------------
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
+  if (warp < 4) {
+    // ---------------- copies: 128 columns of the tile a stage; chunk c of rows 16 g .. 16 g + 15, 16 lanes a row ----------------
+    const int c = lane & 15, r0 = (threadIdx.x >> 4) * 16;
+    const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128);
+    int stage = 0, ready = 0, pending = 0;
+    uint32_t phase = 0;
     bool good = true;
+    auto hand_over = [&]() {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_bar[ready]);
+      if (++ready == S::STAGES) ready = 0;
+      --pending;
+    };
+    int4 ahead[4];   // the next unit's rows
+    int ahead_n = 0;
+    auto look_ahead = [&](int t) {
+      ahead_n = p.plan.info(t).y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ahead[i] = reinterpret_cast<const int4*>(p.plan.rows(t) + r0)[i];
+    };
+    int t = 0, cg = 0;
+    if (u0 < u1) {
+      t = static_cast<int>(u0 % un.tiles);
+      cg = static_cast<int>(u0 / un.tiles);
+      look_ahead(t);
+    }
     for (int64_t u = u0; good && u < u1; ++u) {
-      const int cg = static_cast<int>(u / un.tiles), t = static_cast<int>(u % un.tiles);
       const int side = cg >= un.cg0;
       const int64_t c0 = static_cast<int64_t>(cg - (side ? un.cg0 : 0)) * LORA_WG_COLS;
-      const int groups = (p.plan.info(t).y + 15) / 16 * 4;   // whole steps of 16 rows; rows past the count read as zeros
-      const int4 r4 = reinterpret_cast<const int4*>(p.plan.rows(t))[lane];
-      for (int g = 0; g < 2 && c0 + g * 128 < (side ? p.cols[1] : p.cols[0]); ++g) {
-        if (lane == 0) {
-          good = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag);
-          if (good) mbar_arrive_expect_tx(&full_bar[stage], static_cast<uint32_t>(2 * groups * 512));
-        }
-        good = __shfl_sync(0xffffffffu, good, 0);
+      const int64_t C = (side ? p.cols[1] : p.cols[0]);
+      const uint16_t* X = side ? p.X[1] : p.X[0];
+      const int n16 = (ahead_n + 15) / 16 * 16;   // whole steps of 16 rows; rows past the count are zeros
+      int rows[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rows[4 * i] = ahead[i].x; rows[4 * i + 1] = ahead[i].y; rows[4 * i + 2] = ahead[i].z; rows[4 * i + 3] = ahead[i].w;
+      }
+      if (++t == un.tiles) {
+        t = 0;
+        ++cg;
+      }
+      if (u + 1 < u1) look_ahead(t);
+      for (int g = 0; g < 2 && c0 + g * 128 < C; ++g) {
+        good = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
         if (!good) break;
-        if (lane < groups) {
-          const int c = static_cast<int>(c0) + g * 128;
-          tma_gather4(sX(stage) + lane * 512, side ? &tm1 : &tm0, &full_bar[stage], c, r4);
-          tma_gather4(sX(stage) + LORA_TILE * 128 + lane * 512, side ? &tm1 : &tm0, &full_bar[stage], c + 64, r4);
+        if (r0 < n16) {
+          const uint32_t d = smem_u32(sX(stage)) + off;
+          const int64_t col = c0 + g * 128 + 8 * c;
+          const bool in = col < C;
+          const uint16_t* x = X + (in ? col : 0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const bool on = in && rows[i] < p.plan.M;
+            cp_async16_or_zero(d + 128u * i + (((c & 7) ^ (i & 7)) << 4), x + (on ? rows[i] * C : 0), on);
+          }
         }
-        issued |= 1u << stage;
+        cp_async_commit();
+        if (++pending > S::AHEAD) {
+          cp_async_wait<S::AHEAD>();
+          hand_over();
+        }
         if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (!good && lane == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
-  } else if (warp == 1) {
+    cp_async_wait<0>();
+    if (good)
+      while (pending > 0) hand_over();
+  } else if (warp == 4) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16(128, RB * 64, true) | IDESC_A_MN | IDESC_B_MN;
@@ -887,7 +1052,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
       }
       drain_mma(drain_bar);
     }
-  } else if (warp < 6) {
+  } else if (warp < 9) {
     // ---------------- epilogue, once per segment ----------------
     const int q = warp & 3;
     int acc = 0;
@@ -941,27 +1106,46 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
     }
   } else {
     // ---------------- G's parts, one tile a unit ----------------
-    const int ct = threadIdx.x - 32 * 6;
+    const int ct = threadIdx.x - 32 * 9;
     constexpr int CH = RB * 8;                                          // 8-value chunks of a row
     constexpr int PER = LORA_TILE * CH / (32 * LORA_WG_CONV_WARPS);    // chunks of a thread
     int gb = 0;
     uint32_t g_phase = 0;
+    int t = 0, cg = 0, n = 0;
+    int row[PER];   // the thread's rows of a unit, looked up a unit ahead; -1 past the count
+    auto look_up = [&]() {
+      n = p.plan.info(t).y;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int r = (i * 32 * LORA_WG_CONV_WARPS + ct) / CH;
+        row[i] = p.plan.rows(t)[r];
+        if (r >= n) row[i] = -1;
+      }
+    };
+    if (u0 < u1) {
+      t = static_cast<int>(u0 % un.tiles);
+      cg = static_cast<int>(u0 / un.tiles);
+      look_up();
+    }
     for (int64_t u = u0; u < u1; ++u) {
-      const int cg = static_cast<int>(u / un.tiles), t = static_cast<int>(u % un.tiles);
       const float* G = cg >= un.cg0 ? p.G[1] : p.G[0];
-      const int n = p.plan.info(t).y, n16 = (n + 15) / 16 * 16;
-      const int* rows = p.plan.rows(t);
+      const int n16 = (n + 15) / 16 * 16;
       float4 x[PER][2];
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 * LORA_WG_CONV_WARPS + ct, r = e / CH, c = e % CH;
+        const int c = (i * 32 * LORA_WG_CONV_WARPS + ct) % CH;
         x[i][0] = x[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r < n && 8 * c < p.R) {
-          const float4* src = reinterpret_cast<const float4*>(G + static_cast<int64_t>(rows[r]) * p.R + 8 * c);
+        if (row[i] >= 0 && 8 * c < p.R) {
+          const float4* src = reinterpret_cast<const float4*>(G + static_cast<int64_t>(row[i]) * p.R + 8 * c);
           x[i][0] = src[0];
           x[i][1] = src[1];
         }
       }
+      if (++t == un.tiles) {
+        t = 0;
+        ++cg;
+      }
+      if (u + 1 < u1) look_up();
       if (!mbar_wait(&gempty_bar[gb], g_phase ^ 1u, abort_flag)) break;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
@@ -982,7 +1166,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
     }
   }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 4) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, TCOLS);
@@ -990,45 +1174,46 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1)
 }
 
 // The segments k_lora_wgrad cut between CTAs, added in CTA order, and zeros
-// for adapters without rows. One item is 8 values of R of 256 columns.
+// for adapters without rows. A CTA takes 8 values of R of a segment's 256 columns.
 __global__ void __launch_bounds__(LORA_WG_COLS) k_lora_wgrad_join(const LoraWgradParams p) {
   using T = __nv_bfloat16;
   griddep_wait();
   const LoraWgradUnits un(p);
-  const int rg = p.R / 8;
-  const int64_t items = static_cast<int64_t>(un.cgs) * p.plan.L * rg;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int r0 = static_cast<int>(it % rg) * 8;
-    const int a = static_cast<int>(it / rg % p.plan.L), cg = static_cast<int>(it / rg / p.plan.L);
+  const uint32_t L = static_cast<uint32_t>(p.plan.L);
+  const uint32_t segments = static_cast<uint32_t>(un.cgs) * L;
+  const bool any = un.tiles > 0;
+  for (uint32_t sg = blockIdx.x; sg < segments; sg += gridDim.x) {
+    const int a = static_cast<int>(sg % L), cg = static_cast<int>(sg / L);
     const int side = cg >= un.cg0;
     const int64_t C = (side ? p.cols[1] : p.cols[0]), col = static_cast<int64_t>(cg - (side ? un.cg0 : 0)) * LORA_WG_COLS + threadIdx.x;
-    int t0 = 0, t1 = 0;
-    if (un.tiles > 0) {
-      t0 = p.plan.tile0()[a];
-      t1 = p.plan.tile0()[a + 1];
-    }
-    float f[8] = {};
+    const int t0 = any ? p.plan.tile0()[a] : 0, t1 = any ? p.plan.tile0()[a + 1] : 0;
+    int c0 = 0, c1 = -1;   // CTAs that hold parts of the segment
+    int64_t s0 = 0;
     if (t0 < t1) {
-      const int64_t s0 = static_cast<int64_t>(cg) * un.tiles + t0, s1 = static_cast<int64_t>(cg) * un.tiles + t1;
-      const int c0 = un.owner(s0), c1 = un.owner(s1 - 1);
+      s0 = static_cast<int64_t>(cg) * un.tiles + t0;
+      c0 = un.owner(s0);
+      c1 = un.owner(s0 + (t1 - t0) - 1);
       if (c0 == c1) continue;   // one CTA had it whole
-      if (col < C) {
-        for (int c = c0; c <= c1; ++c) {
-          const float* part = p.part + (static_cast<int64_t>(c) * 2 + (un.first(c) <= s0 ? 1 : 0)) * p.R * LORA_WG_COLS;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] += part[(r0 + i) * LORA_WG_COLS + threadIdx.x];
-        }
-      }
     }
     if (col >= C) continue;
-    if (side == 0) {
+    const float s = side ? __ldg(p.scale + a) : 1.0f;
+    for (int r0 = static_cast<int>(blockIdx.y) * 8; r0 < p.R; r0 += static_cast<int>(gridDim.y) * 8) {
+      float f[8] = {};
+      for (int c = c0; c <= c1; ++c) {
+        const float* part = p.part + (static_cast<int64_t>(c) * 2 + (un.first(c) <= s0 ? 1 : 0)) * p.R * LORA_WG_COLS;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p.out[0][(static_cast<int64_t>(a) * p.R + r0 + i) * C + col] = from_f<T>(f[i]);
-    } else {
-      const float s = __ldg(p.scale + a);
-      *reinterpret_cast<uint4*>(p.out[1] + (static_cast<int64_t>(a) * C + col) * p.R + r0) =
-          make_uint4(pack2<T>(t0 < t1 ? f[0] * s : 0.0f, t0 < t1 ? f[1] * s : 0.0f), pack2<T>(t0 < t1 ? f[2] * s : 0.0f, t0 < t1 ? f[3] * s : 0.0f),
-                     pack2<T>(t0 < t1 ? f[4] * s : 0.0f, t0 < t1 ? f[5] * s : 0.0f), pack2<T>(t0 < t1 ? f[6] * s : 0.0f, t0 < t1 ? f[7] * s : 0.0f));
+        for (int i = 0; i < 8; ++i) f[i] += part[(r0 + i) * LORA_WG_COLS + threadIdx.x];
+      }
+      if (side == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.out[0][(static_cast<int64_t>(a) * p.R + r0 + i) * C + col] = from_f<T>(f[i]);
+      } else {
+        if (c1 >= c0) {   // else zeros, whatever the scale
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= s;
+        }
+        *reinterpret_cast<uint4*>(p.out[1] + (static_cast<int64_t>(a) * C + col) * p.R + r0) = narrow8<T>(f);
+      }
     }
   }
 }

@@ -63,19 +63,6 @@ __device__ __forceinline__ float cta_reduce(float v, float (*red)[16], int& slot
   return t;
 }
 
-template <typename T>
-__device__ __forceinline__ void widen8(const uint4& u, float (&f)[8]) {
-  uint16_t h[8];
-  unpack8(u, h);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = to_f<T>(h[i]);
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
-  return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-}
-
 // One row at a time per CTA, V 16-byte vectors of it per thread; the CTAs
 // stride over the rows. gamma and beta stay in registers when a thread holds
 // at most four vectors of them.

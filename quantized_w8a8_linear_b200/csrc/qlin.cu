@@ -1376,9 +1376,9 @@ qlin_status allow_smem(Kern kern, int bytes, std::atomic<bool> (&set)[16]) {
 
 // A launch as a programmatic dependent of the kernel before it, in clusters of `cluster` CTAs.
 template <typename... P, typename... A>
-qlin_status launch_dependent(void (*kern)(P...), const char* what, int64_t grid, int threads, int smem, int cluster, cudaStream_t st, A&&... args) {
+qlin_status launch_dependent(void (*kern)(P...), const char* what, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
@@ -1462,7 +1462,7 @@ qlin_status norm_bwd(const NormBwdArgs& a, void* dgamma, void* dbeta, cudaStream
   else QLIN_NORM_BWD(4);
 #undef QLIN_NORM_BWD
   if (s != QLIN_OK || a.part == nullptr) return s;
-  return launch_dependent(k_norm_bwd_cols<T>, "k_norm_bwd_cols launch", 2 * a.K / 32, 512, 0, 1, st, static_cast<const float*>(a.part), a.K,
+  return launch_dependent(k_norm_bwd_cols<T>, "k_norm_bwd_cols launch", dim3(static_cast<unsigned>(2 * a.K / 32)), 512, 0, 1, st, static_cast<const float*>(a.part), a.K,
                           static_cast<int>(ctas), static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
 }
 
@@ -1576,20 +1576,6 @@ namespace {
 constexpr int64_t kLoraMaxM = int64_t{1} << 28;
 constexpr int LORA_WG_MAX_CTAS = 160;
 
-// 16-bit row-major [rows, cols] for row gathers of 64 columns (box one row high), 128B swizzle.
-qlin_status make_tmap_gather(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc;
-  QLIN_TRY(get_encode(&enc));
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * 2)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(LORA_BK), 1u};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(QLIN_ERR_CUDA, "cuTensorMapEncodeTiled (gather) failed (%d)", static_cast<int>(r));
-  return QLIN_OK;
-}
-
 // Adapter weights 16-bit [L, rows, cols]: box 64 columns x box_rows of one
 // adapter, 128B swizzle; rows past `rows` read as zeros, not as the next adapter's.
 qlin_status make_tmap_adapters(CUtensorMap* m, const void* base, int64_t L, int64_t rows, int64_t cols, int box_rows) {
@@ -1617,9 +1603,8 @@ struct LoraCall {
 // H [M,R] = scale * X W^T; X [M,C]. W_MN: W is B [L,C,R], else A [L,R,C].
 template <typename T, int RB, bool W_MN>
 qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H) {
-  CUtensorMap tx, tw;
-  QLIN_TRY(make_tmap_gather(&tx, X, c.M, C));
-  if (W_MN) QLIN_TRY(make_tmap_adapters(&tw, W, c.L, C, c.R, LORA_BK));
+  CUtensorMap tw;
+  if (W_MN) QLIN_TRY(make_tmap_adapters(&tw, W, c.L, C, c.R, LORA_SHRINK_BK));
   else QLIN_TRY(make_tmap_adapters(&tw, W, c.L, c.R, C, static_cast<int>(round_up(c.R, 16))));
   auto kern = k_lora_shrink<T, RB, W_MN>;
   constexpr int smem = LoraShrinkSmem<RB>::TOTAL;
@@ -1629,9 +1614,9 @@ qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, c
   // tiles are full, and that leaves every CTA a block of the contraction
   const int64_t full = (c.M + LORA_TILE - 1) / LORA_TILE;
   int cluster = 8;
-  while (cluster > 1 && (full * cluster > 2 * c.d->sms || cluster > (C + LORA_BK - 1) / LORA_BK)) cluster /= 2;
-  LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), scale, H};
-  return launch_dependent(kern, "k_lora_shrink launch", lora_max_tiles(c.M, c.L) * cluster, LORA_SHRINK_THREADS, smem, cluster, c.st, tx, tw, p, cluster);
+  while (cluster > 1 && (full * cluster > 2 * c.d->sms || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
+  LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), static_cast<const uint16_t*>(X), scale, H};
+  return launch_dependent(kern, "k_lora_shrink launch", dim3(static_cast<unsigned>(lora_max_tiles(c.M, c.L) * cluster)), LORA_SHRINK_THREADS, smem, cluster, c.st, tw, p, cluster);
 }
 template <typename T, bool W_MN>
 qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H) {
@@ -1641,20 +1626,17 @@ qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, cons
 // Y [M,N] += scale * H V^T. V_MN: V is A [L,R,N], else B [L,N,R].
 template <typename T, int RB, bool V_MN, bool VEC>
 qlin_status launch_lora_expand_rb(const LoraCall& c, const float* H, const void* V, int64_t N, const float* scale, void* Y) {
-  CUtensorMap tv, ty;
+  CUtensorMap tv;
   if (V_MN) QLIN_TRY(make_tmap_adapters(&tv, V, c.L, c.R, N, static_cast<int>(round_up(c.R, 16))));
   else QLIN_TRY(make_tmap_adapters(&tv, V, c.L, N, c.R, LORA_EXPAND_BN));
-  std::memset(&ty, 0, sizeof(ty));
-  if (VEC) QLIN_TRY(make_tmap_gather(&ty, Y, c.M, N));
   auto kern = k_lora_expand<T, RB, V_MN, VEC>;
-  constexpr int smem = LoraExpandSmem<RB, VEC>::TOTAL;
-  static_assert(smem <= 227 * 1024, "k_lora_expand shared memory");
+  constexpr int smem = LoraExpandSmem<RB>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
   const int64_t most = lora_max_tiles(c.M, c.L) * ((N + LORA_EXPAND_BN - 1) / LORA_EXPAND_BN);
-  const int64_t grid = std::min<int64_t>(most, (smem <= 113 * 1024 ? 2 : 1) * c.d->sms);
+  const int64_t grid = std::min<int64_t>(most, c.d->sms);
   LoraExpandParams p{c.view(), N, static_cast<int>(c.R), scale, H, static_cast<uint16_t*>(Y)};
-  return launch_dependent(kern, "k_lora_expand launch", grid, LORA_EXPAND_THREADS, smem, 1, c.st, tv, ty, p);
+  return launch_dependent(kern, "k_lora_expand launch", dim3(static_cast<unsigned>(grid)), LORA_EXPAND_THREADS, smem, 1, c.st, tv, p);
 }
 template <typename T, bool V_MN>
 qlin_status launch_lora_expand(const LoraCall& c, const float* H, const void* V, int64_t N, const float* scale, void* Y) {
@@ -1669,17 +1651,16 @@ int lora_wg_ctas(const DeviceInfo* d) { return std::min(d->sms, LORA_WG_MAX_CTAS
 template <int RB>
 qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const float* dH, void* dA, const void* dY, int64_t N, const float* H,
                               void* dB, float* part) {
-  CUtensorMap t0, t1;
-  QLIN_TRY(make_tmap_gather(&t0, X, c.M, K));
-  QLIN_TRY(make_tmap_gather(&t1, dY, c.M, N));
   auto kern = k_lora_wgrad<RB>;
   constexpr int smem = LoraWgradSmem<RB>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {dH, H}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
-  QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", p.ctas, LORA_WG_THREADS, smem, 1, c.st, t0, t1, p));
-  const int64_t items = ((K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS) * c.L * (c.R / 8);
-  return launch_dependent(k_lora_wgrad_join, "k_lora_wgrad_join launch", std::min<int64_t>(items, 8 * c.d->sms), LORA_WG_COLS, 0, 1, c.st, p);
+  LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dH, H}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
+  QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", dim3(static_cast<unsigned>(p.ctas)), LORA_WG_THREADS, smem, 1, c.st, p));
+  const int64_t segments = ((K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS) * c.L;
+  const int64_t rg = c.R / 8;   // grid.y
+  return launch_dependent(k_lora_wgrad_join, "k_lora_wgrad_join launch", dim3(static_cast<unsigned>(std::min<int64_t>(segments, 8 * c.d->sms)), static_cast<unsigned>(rg)),
+                          LORA_WG_COLS, 0, 1, c.st, p);
 }
 
 qlin_status check_lora(int64_t M, int64_t L, int64_t R, const void* A, const void* B, const float* scale, const void* plan, size_t plan_bytes) {
