@@ -335,7 +335,7 @@ QLIN_API qlin_status qlin_lora_plan(const int32_t *idx, int64_t M, int64_t L, vo
  * for bit. H [M,R] fp32 is written for rows that have one (kept for the
  * backward pass, else scratch). H enters the second product as two 16-bit
  * parts (16 significant bits in bf16, 22 in fp16); all sums are fp32 and Y is
- * rounded once. R % 8 == 0, 8 <= R <= 128; N is arbitrary. A row's result does
+ * rounded once. R % 8 == 0, 8 <= R <= 128; N is arbitrary up to 2^28. A row's result does
  * not depend on the other rows of the batch beyond the order in which its K
  * products are added. */
 QLIN_API qlin_status qlin_lora_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A, const void *B,

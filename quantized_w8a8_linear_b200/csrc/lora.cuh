@@ -148,7 +148,10 @@ __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx,
 // ---------------------------------------------------------------------------
 // helpers
 // ---------------------------------------------------------------------------
-// 16-byte asynchronous global -> shared copy, or 16 zero bytes.
+// Bytes from a matrix's start to its row; rows are below 2^28 and their size below 2^30 bytes, so one multiply-add does.
+__device__ __forceinline__ int64_t row_bytes(int row, int bytes) { return static_cast<int64_t>(row) * bytes; }
+
+// 16-byte asynchronous global -> shared copy, or 16 zero bytes (`src` is then not read).
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(copy ? 16 : 0) : "memory");
 }
@@ -244,6 +247,16 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo
   lo = make_uint4(l[0] | (l[1] << 16), l[2] | (l[3] << 16), l[4] | (l[5] << 16), l[6] | (l[7] << 16));
 }
 
+// The same for 4 values, written to row[0] and row[R] of a split row [2][R].
+template <typename T>
+__device__ __forceinline__ void store_split4(uint16_t* row, int R, const float4& v) {
+  const float f[8] = {v.x, v.y, v.z, v.w};
+  uint4 hi, lo;
+  split8<T>(f, hi, lo);
+  *reinterpret_cast<uint2*>(row) = make_uint2(hi.x, hi.y);
+  *reinterpret_cast<uint2*>(row + R) = make_uint2(lo.x, lo.y);
+}
+
 // ---------------------------------------------------------------------------
 // k_lora_shrink: H[rows of the tile] = X W^T (c partial sums over the
 // contraction, one per CTA of a cluster).
@@ -253,6 +266,8 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo
 // fp32 partial tiles meet in shared memory and CTA q adds rows q, q + c, ...
 // of all of them in rank order (distributed shared memory; no workspace and
 // no second kernel). c is chosen so that few tiles still fill the SMs.
+// In the backward pass (W_MN 1) it also leaves dH and the forward's H as split
+// rows [2][R] for k_lora_wgrad, whose every CTA reads all of them.
 // ---------------------------------------------------------------------------
 constexpr int LORA_SHRINK_THREADS = 160;   // warps 0-3 copies, then the epilogue; warp 4 MMA
 constexpr int LORA_SHRINK_BK = 128;        // contraction of a stage: 256 bytes of a row
@@ -264,12 +279,15 @@ struct LoraShrinkParams {
   const uint16_t* X;    // [M,C]
   const float* scale;   // [L], or nullptr: 1
   float* H;             // [M,R]
+  // W_MN 1:
+  uint16_t* Hs;         // [M,2,R] the parts of H
+  const float* G;       // [M,R] another matrix to split
+  uint16_t* Gs;         // [M,2,R]
 };
 
 template <int RB>   // ceil(R / 64)
 struct LoraShrinkSmem {
   static constexpr int STAGES = RB == 1 ? 2 : 3;   // two CTAs an SM, or one
-  static constexpr int AHEAD = STAGES - 1;          // stages a thread's copies run ahead of the one it hands over
   static constexpr int A_BYTES = 2 * LORA_TILE * 128;   // two halves of 64 columns
   static constexpr int W_BYTES = 2 * RB * 64 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(&full_bar[s], 5);   // four copying warps, and the copy of W
+      mbar_init(&full_bar[s], 129);   // the copying threads, and the copy of W
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(tfull_bar, 1);
@@ -336,16 +354,11 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     int src[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) src[i] = r0 + 8 * i < n ? rows[r0 + 8 * i] : -1;
+    const int C = static_cast<int>(p.C);
     const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128 + (((c & 7) ^ r0) << 4));
-    int stage = 0, ready = 0;
+    int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool good = true;
-    auto hand_over = [&]() {   // the oldest stage not handed over: this thread's copies of it have landed
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full_bar[ready]);
-      if (++ready == S::STAGES) ready = 0;
-    };
     for (int kb = kb0; kb < kb1; ++kb) {
       good = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
       if (!good) break;
@@ -360,25 +373,18 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
         }
       }
       const uint32_t d = smem_u32(sA(stage)) + off;
-      const bool in = kb * LORA_SHRINK_BK + 8 * c < p.C;
-      const uint16_t* x = p.X + (in ? kb * LORA_SHRINK_BK + 8 * c : 0);
+      const bool in = kb * LORA_SHRINK_BK + 8 * c < C;
+      const uint8_t* x = reinterpret_cast<const uint8_t*>(p.X + kb * LORA_SHRINK_BK + 8 * c);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (src[i] >= 0) cp_async16_or_zero(d + 1024u * i, x + src[i] * p.C, in);
-      cp_async_commit();
+        if (src[i] >= 0) cp_async16_or_zero(d + 1024u * i, x + row_bytes(src[i], 2 * C), in);
+      cp_async_arrive(&full_bar[stage]);
       issued |= 1u << stage;
-      if (kb - kb0 >= S::AHEAD) {
-        cp_async_wait<S::AHEAD>();
-        hand_over();
-      }
       if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
     }
+    cp_async_commit();
     cp_async_wait<0>();
-    if (good) {
-      for (int i = kb1 - kb0 < S::AHEAD ? kb1 - kb0 : S::AHEAD; i > 0; --i) hand_over();
-    } else if (threadIdx.x == 0) {
-      drain_ring(full_bar, S::STAGES, stage, phase, issued);
-    }
+    if (!good && threadIdx.x == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
     // ---------------- epilogue: row q * 32 + lane of the tile ----------------
     const int q = warp;
     const int r = q * 32 + lane;
@@ -398,7 +404,10 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
             if (c0 + i < p.R) {
               float4 f = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
               if (!good) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (cluster == 1) f = make_float4(f.x * s, f.y * s, f.z * s, f.w * s);
+              if (cluster == 1) {
+                f = make_float4(f.x * s, f.y * s, f.z * s, f.w * s);
+                if constexpr (W_MN) store_split4<T>(p.Hs + static_cast<int64_t>(rows[r]) * 2 * p.R + c0 + i, p.R, f);
+              }
               *reinterpret_cast<float4*>(out + c0 + i) = f;
             }
           }
@@ -414,6 +423,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait(&full_bar[stage], phase, abort_flag)) break;
+      fence_proxy_async_smem();   // X was written by cp.async, through the generic proxy
       tc_fence_after();
       const uint32_t as = smem_u32(sA(stage)), ws = smem_u32(sW(stage));
 #pragma unroll
@@ -442,11 +452,21 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
           const float4 f = ld_cluster_f4(base + static_cast<uint32_t>((r * (Rp + 4) + c) * 4), k);
           sum = make_float4(sum.x + f.x, sum.y + f.y, sum.z + f.z, sum.w + f.w);
         }
-        *reinterpret_cast<float4*>(p.H + static_cast<int64_t>(p.plan.rows(tile)[r]) * p.R + c) =
-            make_float4(sum.x * s, sum.y * s, sum.z * s, sum.w * s);
+        sum = make_float4(sum.x * s, sum.y * s, sum.z * s, sum.w * s);
+        const int64_t row = p.plan.rows(tile)[r];
+        *reinterpret_cast<float4*>(p.H + row * p.R + c) = sum;
+        if constexpr (W_MN) store_split4<T>(p.Hs + row * 2 * p.R + c, p.R, sum);
       }
     }
     cluster_sync();   // no CTA leaves while another reads its partial tile
+  }
+  if constexpr (W_MN) {
+    const int r4 = p.R / 4, mine = rank < n ? (n - rank + cluster - 1) / cluster : 0;
+    for (int e = threadIdx.x; e < mine * r4; e += LORA_SHRINK_THREADS) {
+      const int64_t row = p.plan.rows(tile)[rank + e / r4 * cluster];
+      const int c = e % r4 * 4;
+      store_split4<T>(p.Gs + row * 2 * p.R + c, p.R, *reinterpret_cast<const float4*>(p.G + row * p.R + c));
+    }
   }
   __syncthreads();
   if (warp == 4) {
@@ -558,7 +578,6 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
   const int64_t units = static_cast<int64_t>(p.plan.tiles()) * nbs;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   const int t0 = static_cast<int>(u0 / nbs), nb0 = static_cast<int>(u0 % nbs);   // first tile and columns
-  const int Rp = (p.R + 15) / 16 * 16;
   // byte of its aligned 16-byte chunk at which the piece of `row` from column n0 starts
   auto shift_of = [&](int64_t row, int64_t n0) { return VEC ? 0 : static_cast<int>((2 * (row * p.N + n0)) & 15); };
 
@@ -566,6 +585,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     // ---------------- copies of Y: chunk c of rows r0, r0 + 8, ..., 16 lanes a row ----------------
     const int c = lane & 15, r0 = threadIdx.x >> 4;
     const int64_t all = 2 * p.plan.M * p.N;   // bytes of Y
+    const int row_size = static_cast<int>(2 * p.N);
     const uint8_t* Y = reinterpret_cast<const uint8_t*>(p.Y);
     int rows[16];
     int stage = 0, n = 0;
@@ -579,13 +599,13 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
       }
       good = __all_sync(0xffffffffu, mbar_wait(&yempty_bar[stage], phase ^ 1u, abort_flag));
       if (!good) break;
-      const int64_t n0 = nb * LORA_EXPAND_BN;
+      const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
       const int bytes = static_cast<int>(2 * (p.N - n0 < LORA_EXPAND_BN ? p.N - n0 : LORA_EXPAND_BN));
       const uint32_t d = smem_u32(sY(stage)) + r0 * S::Y_ROW;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (rows[i] >= 0) {
-          const int64_t b = 2 * (rows[i] * p.N + n0);
+          const int64_t b = row_bytes(rows[i], row_size) + 2 * n0;
           const int shift = VEC ? 0 : static_cast<int>(b & 15);
           const int64_t at = b - shift + 16 * c;
           if (16 * c < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i + 16 * c, Y + at, VEC ? 16 : all - at);
@@ -613,10 +633,10 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
         const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
         good = mbar_wait(&vempty_bar[stage], phase ^ 1u, abort_flag);
         if (!good) break;
-        mbar_arrive_expect_tx(&vfull_bar[stage], static_cast<uint32_t>(V_MN ? 2 * Rp * 128 : S::V_BYTES));
+        mbar_arrive_expect_tx(&vfull_bar[stage], S::V_BYTES);
         if constexpr (V_MN) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) tma_load_3d(sV(stage) + h * Rp * 128, &tmV, &vfull_bar[stage], n0 + 64 * h, 0, a);
+          for (int h = 0; h < 2; ++h) tma_load_3d(sV(stage) + h * (RB * 64 * 128), &tmV, &vfull_bar[stage], n0 + 64 * h, 0, a);
         } else {
 #pragma unroll
           for (int b = 0; b < RB; ++b) tma_load_3d(sV(stage) + b * (LORA_EXPAND_BN * 128), &tmV, &vfull_bar[stage], b * 64, n0, a);
@@ -634,7 +654,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16(LORA_TILE, LORA_EXPAND_BN, std::is_same<T, __nv_bfloat16>::value) | (V_MN ? IDESC_B_MN : 0u);
-      const int ksteps = Rp / 16;
+      constexpr int KS = 4 * RB;
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, h_phase = 0;
       bool next = true;
@@ -648,12 +668,12 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * LORA_EXPAND_BN);
         const uint32_t v = smem_u32(sV(stage)), h = smem_u32(sH);
-        for (int part = 0; part < 2; ++part) {
-          for (int k = 0; k < ksteps; ++k) {
-            const uint64_t adesc = sdesc_k128(h + part * S::H_BYTES + (k >> 2) * (LORA_TILE * 128)) + 2u * (k & 3);
-            const uint64_t bdesc = V_MN ? sdesc_mn128(v, static_cast<uint32_t>(Rp * 128)) + 128u * k : sdesc_k128(v + (k >> 2) * (LORA_EXPAND_BN * 128)) + 2u * (k & 3);
-            umma<2>(d, adesc, bdesc, idesc, (part | k) != 0 ? 1u : 0u);
-          }
+#pragma unroll
+        for (int k = 0; k < 2 * KS; ++k) {   // both parts of H; zeros past R
+          const int i = k % KS;
+          const uint64_t adesc = sdesc_k128(h + (k / KS) * S::H_BYTES + (i >> 2) * (LORA_TILE * 128)) + 2u * (i & 3);
+          const uint64_t bdesc = V_MN ? sdesc_mn128(v, KS * 2048u) + 128u * i : sdesc_k128(v + (i >> 2) * (LORA_EXPAND_BN * 128)) + 2u * (i & 3);
+          umma<2>(d, adesc, bdesc, idesc, k != 0 ? 1u : 0u);
         }
         umma_commit(&vempty_bar[stage]);
         umma_commit(&tfull_bar[acc]);
@@ -742,7 +762,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
       acc_phase ^= 1u;
       tc_fence_after();
       if (n > 0) {
-        const int64_t n0 = nb * LORA_EXPAND_BN;
+        const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
         uint8_t* yr = sY(stage) + q * 32 * S::Y_ROW;   // the warp's rows
         const int shift = shift_of(my_row, n0);
         uint8_t* mine = yr + lane * S::Y_ROW + 128 * half + (VEC ? 0 : shift & ~3);
@@ -787,19 +807,19 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
         if (lane == 0) mbar_arrive(&tempty_bar[group]);   // the accumulator is in shared memory
         // out: eight lanes a row, 16-byte chunk c of the warp's 128 bytes of it
         const int c = lane & 7;
-        const int64_t col = n0 + 64 * half;
+        const int N = static_cast<int>(p.N), col = n0 + 64 * half;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = i * 4 + (lane >> 3);
-          const int64_t row = __shfl_sync(0xffffffffu, my_row, r);
+          const int row = __shfl_sync(0xffffffffu, my_row, r);
           if (r < n) {
             const uint8_t* src = yr + r * S::Y_ROW + 128 * half;
-            uint8_t* dst = reinterpret_cast<uint8_t*>(p.Y + row * p.N + col);
+            uint8_t* dst = reinterpret_cast<uint8_t*>(p.Y + col) + row_bytes(row, 2 * N);
             if constexpr (VEC) {
-              if (col + 8 * c < p.N) *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(src + 16 * c);
+              if (col + 8 * c < N) *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(src + 16 * c);
             } else {
               const int sh = shift_of(row, n0);
-              const int cols = p.N - col < 64 ? static_cast<int>(p.N - col) : 64;
+              const int cols = N - col < 64 ? N - col : 64;
               // elements [e0, e0 + 8) of the warp's 64 lie in one chunk; with a shift, the last lane has the first and last pieces
               const int e0 = sh == 0 ? 8 * c : 8 * c + (16 - sh) / 2;
               if (e0 + 8 <= 64 && e0 + 8 <= cols) {
@@ -852,16 +872,16 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
 // bf16 only: G's parts need fp32's exponent range (a power of two per row, as
 // k_lora_expand takes out, does not leave a sum over rows).
 // ---------------------------------------------------------------------------
-constexpr int LORA_WG_THREADS = 544;   // warps 0-3 copies, warp 4 MMA, warps 5-8 epilogue, warps 9-16 split G
-constexpr int LORA_WG_CONV_WARPS = 8;
+constexpr int LORA_WG_THREADS = 416;   // warps 0-3 copy X, warp 4 MMA, warps 5-8 epilogue, warps 9-12 copy G
 constexpr int LORA_WG_COLS = 256;      // columns of a unit: two MMAs of M = 128
+constexpr int LORA_WG_ROWS = 64;       // rows of a block of MMAs: a tile has one or two
 
 struct LoraWgradParams {
   LoraPlan plan;
   int R, ctas;
   int64_t cols[2];       // K, N
   const uint16_t* X[2];  // X [M,K], dY [M,N]
-  const float* G[2];     // dH, H [M,R]
+  const uint16_t* G[2];  // dH, H as split rows [M,2,R]
   const float* scale;    // [L]
   uint16_t* out[2];      // dA [L,R,K], dB [L,N,R]
   float* part;           // [ctas][2][R][256] fp32
@@ -885,8 +905,7 @@ struct LoraWgradUnits {
 
 template <int RB>
 struct LoraWgradSmem {
-  static constexpr int STAGES = RB == 1 ? 4 : 3;
-  static constexpr int AHEAD = STAGES - 2;
+  static constexpr int STAGES = RB == 1 ? 5 : 3;
   static constexpr int X_BYTES = 2 * LORA_TILE * 128;            // 128 columns of the tile: two 64-column halves
   static constexpr int G_BYTES = RB * LORA_TILE * 128;           // one part
   static constexpr int BAR_BYTES = 8 * (2 * STAGES + 9) + 16;
@@ -917,11 +936,11 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(&full_bar[s], 4);
+      mbar_init(&full_bar[s], 128);
       mbar_init(&empty_bar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&gfull_bar[b], LORA_WG_CONV_WARPS);
+      mbar_init(&gfull_bar[b], 128);
       mbar_init(&gempty_bar[b], 1);
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], 4);
@@ -945,19 +964,12 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   const int64_t u0 = un.first(blockIdx.x), u1 = un.first(blockIdx.x + 1);
 
   if (warp < 4) {
-    // ---------------- copies: 128 columns of the tile a stage; chunk c of rows 16 g .. 16 g + 15, 16 lanes a row ----------------
+    // ---------------- copies: 128 columns of the tile a stage; chunk c of rows r0 .. r0 + 15, 16 lanes a row ----------------
     const int c = lane & 15, r0 = (threadIdx.x >> 4) * 16;
     const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128);
-    int stage = 0, ready = 0, pending = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool good = true;
-    auto hand_over = [&]() {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full_bar[ready]);
-      if (++ready == S::STAGES) ready = 0;
-      --pending;
-    };
     int4 ahead[4];   // the next unit's rows
     int ahead_n = 0;
     auto look_ahead = [&](int t) {
@@ -974,9 +986,9 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
     for (int64_t u = u0; good && u < u1; ++u) {
       const int side = cg >= un.cg0;
       const int64_t c0 = static_cast<int64_t>(cg - (side ? un.cg0 : 0)) * LORA_WG_COLS;
-      const int64_t C = (side ? p.cols[1] : p.cols[0]);
+      const int C = static_cast<int>(side ? p.cols[1] : p.cols[0]);
       const uint16_t* X = side ? p.X[1] : p.X[0];
-      const int n16 = (ahead_n + 15) / 16 * 16;   // whole steps of 16 rows; rows past the count are zeros
+      const int rows_in = (ahead_n + LORA_WG_ROWS - 1) / LORA_WG_ROWS * LORA_WG_ROWS;   // rows past the count are zeros, up to the next MMA block
       int rows[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -990,28 +1002,21 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       for (int g = 0; g < 2 && c0 + g * 128 < C; ++g) {
         good = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
         if (!good) break;
-        if (r0 < n16) {
-          const uint32_t d = smem_u32(sX(stage)) + off;
-          const int64_t col = c0 + g * 128 + 8 * c;
-          const bool in = col < C;
-          const uint16_t* x = X + (in ? col : 0);
+        const uint32_t d = smem_u32(sX(stage)) + off;
+        const int col = static_cast<int>(c0) + g * 128 + 8 * c;
+        const int most = col < C ? static_cast<int>(p.plan.M) : 0;   // rows from here on are zeros
+        const uint8_t* x = reinterpret_cast<const uint8_t*>(X + col);
+        if (r0 < rows_in) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const bool on = in && rows[i] < p.plan.M;
-            cp_async16_or_zero(d + 128u * i + (((c & 7) ^ (i & 7)) << 4), x + (on ? rows[i] * C : 0), on);
-          }
+          for (int i = 0; i < 16; ++i)
+            cp_async16_or_zero(d + 128u * i + (((c & 7) ^ (i & 7)) << 4), x + row_bytes(rows[i], 2 * C), rows[i] < most);
         }
-        cp_async_commit();
-        if (++pending > S::AHEAD) {
-          cp_async_wait<S::AHEAD>();
-          hand_over();
-        }
+        cp_async_arrive(&full_bar[stage]);
         if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
       }
     }
+    cp_async_commit();
     cp_async_wait<0>();
-    if (good)
-      while (pending > 0) hand_over();
   } else if (warp == 4) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
@@ -1019,24 +1024,41 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       int stage = 0, gb = 0, acc = 0;
       uint32_t phase = 0, g_phase = 0, acc_phase = 0;
       bool good = true, open = false;
+      int t = 0, cg = 0;
+      int2 info = make_int2(0, 0);
+      if (u0 < u1) {
+        t = static_cast<int>(u0 % un.tiles);
+        cg = static_cast<int>(u0 / un.tiles);
+        info = p.plan.info(t);
+      }
       for (int64_t u = u0; good && u < u1; ++u) {
-        const int cg = static_cast<int>(u / un.tiles), t = static_cast<int>(u % un.tiles);
         const int side = cg >= un.cg0;
         const int64_t c0 = static_cast<int64_t>(cg - (side ? un.cg0 : 0)) * LORA_WG_COLS;
-        const int2 info = p.plan.info(t);
-        const int ksteps = (info.y + 15) / 16;
+        const int2 here = info;
+        const bool last = ++t == un.tiles;   // of these columns
+        if (last) {
+          t = 0;
+          ++cg;
+        }
+        if (u + 1 < u1) info = p.plan.info(t);   // looked up a unit ahead
         if (!open && !mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag)) break;
         if (!mbar_wait(&gfull_bar[gb], g_phase, abort_flag)) break;
         const uint32_t gs = smem_u32(sG(gb));
-        for (int g = 0; g < 2 && c0 + g * 128 < (side ? p.cols[1] : p.cols[0]); ++g) {
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { good = false; break; }
-          tc_fence_after();
+        for (int g = 0; good && g < 2 && c0 + g * 128 < (side ? p.cols[1] : p.cols[0]); ++g) {
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g * RB * 64);
-          const uint64_t adesc = sdesc_mn128(smem_u32(sX(stage)), LORA_TILE * 128);
-          for (int part = 0; part < 2; ++part) {
-            const uint64_t bdesc = sdesc_mn128(gs + part * S::G_BYTES, LORA_TILE * 128);
-            for (int k = 0; k < ksteps; ++k)
-              umma<2>(d, adesc + 128u * k, bdesc + 128u * k, idesc, (open || (part | k) != 0) ? 1u : 0u);
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { good = false; break; }
+          fence_proxy_async_smem();   // X and G were written by cp.async, through the generic proxy
+          tc_fence_after();
+          constexpr int KS = LORA_WG_ROWS / 16;
+#pragma unroll
+          for (int h = 0; h < LORA_TILE / LORA_WG_ROWS; ++h) {
+            if (LORA_WG_ROWS * h >= here.y) break;
+            const uint64_t adesc = sdesc_mn128(smem_u32(sX(stage)) + h * (LORA_WG_ROWS * 128), LORA_TILE * 128);
+            const uint64_t bdesc = sdesc_mn128(gs + h * (LORA_WG_ROWS * 128), LORA_TILE * 128);
+            const uint32_t more = open || h > 0 ? 1u : 0u;
+#pragma unroll
+            for (int k = 0; k < 2 * KS; ++k)   // both parts of G
+              umma<2>(d, adesc + 128u * (k % KS), bdesc + 128u * (k % KS) + (k / KS) * (S::G_BYTES >> 4), idesc, k == 0 ? more : 1u);
           }
           umma_commit(&empty_bar[stage]);
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
@@ -1044,7 +1066,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
         if (!good) break;
         umma_commit(&gempty_bar[gb]);
         if (++gb == 2) { gb = 0; g_phase ^= 1u; }
-        open = u + 1 < u1 && t + 1 < p.plan.tile0()[info.x + 1];
+        open = u + 1 < u1 && !last && info.x == here.x;
         if (!open) {
           umma_commit(&tfull_bar[acc]);
           if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
@@ -1105,21 +1127,21 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       u = seg1 < u1 ? seg1 : u1;
     }
   } else {
-    // ---------------- G's parts, one tile a unit ----------------
+    // ---------------- copies of G's parts, one tile a unit: chunk c of rows r0, r0 + step, ... of both parts ----------------
+    constexpr int CH = RB * 8;                 // 16-byte chunks of a row of a part
+    constexpr int STEP = 128 / CH, PER = LORA_TILE / STEP;
     const int ct = threadIdx.x - 32 * 9;
-    constexpr int CH = RB * 8;                                          // 8-value chunks of a row
-    constexpr int PER = LORA_TILE * CH / (32 * LORA_WG_CONV_WARPS);    // chunks of a thread
-    int gb = 0;
+    const int c = ct % CH, r0 = ct / CH;
+    const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128);
+    int gb = 0, t = 0, cg = 0, n = 0;
     uint32_t g_phase = 0;
-    int t = 0, cg = 0, n = 0;
     int row[PER];   // the thread's rows of a unit, looked up a unit ahead; -1 past the count
     auto look_up = [&]() {
       n = p.plan.info(t).y;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int r = (i * 32 * LORA_WG_CONV_WARPS + ct) / CH;
-        row[i] = p.plan.rows(t)[r];
-        if (r >= n) row[i] = -1;
+        row[i] = p.plan.rows(t)[r0 + STEP * i];
+        if (r0 + STEP * i >= n) row[i] = -1;
       }
     };
     if (u0 < u1) {
@@ -1128,42 +1150,31 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       look_up();
     }
     for (int64_t u = u0; u < u1; ++u) {
-      const float* G = cg >= un.cg0 ? p.G[1] : p.G[0];
-      const int n16 = (n + 15) / 16 * 16;
-      float4 x[PER][2];
+      const uint16_t* G = cg >= un.cg0 ? p.G[1] : p.G[0];
+      const int n64 = (n + LORA_WG_ROWS - 1) / LORA_WG_ROWS * LORA_WG_ROWS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&gempty_bar[gb], g_phase ^ 1u, abort_flag))) break;
+      const uint32_t d = smem_u32(sG(gb)) + off;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int c = (i * 32 * LORA_WG_CONV_WARPS + ct) % CH;
-        x[i][0] = x[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row[i] >= 0 && 8 * c < p.R) {
-          const float4* src = reinterpret_cast<const float4*>(G + static_cast<int64_t>(row[i]) * p.R + 8 * c);
-          x[i][0] = src[0];
-          x[i][1] = src[1];
+        const int r = r0 + STEP * i;
+        if (r < n64) {
+          const bool on = row[i] >= 0 && 8 * c < p.R;
+          const uint16_t* src = G + row_bytes(row[i], 2 * p.R) + 8 * c;   // in elements
+          const uint32_t at = d + 128u * STEP * i + (((c & 7) ^ (r & 7)) << 4);
+          cp_async16_or_zero(at, src, on);
+          cp_async16_or_zero(at + S::G_BYTES, src + p.R, on);
         }
       }
+      cp_async_arrive(&gfull_bar[gb]);
       if (++t == un.tiles) {
         t = 0;
         ++cg;
       }
       if (u + 1 < u1) look_up();
-      if (!mbar_wait(&gempty_bar[gb], g_phase ^ 1u, abort_flag)) break;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 * LORA_WG_CONV_WARPS + ct, r = e / CH, c = e % CH;
-        if (r < n16) {
-          const float f[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-          uint4 hi, lo;
-          split8<T>(f, hi, lo);
-          uint8_t* d = sG(gb) + (c >> 3) * (LORA_TILE * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(d) = hi;
-          *reinterpret_cast<uint4*>(d + S::G_BYTES) = lo;
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&gfull_bar[gb]);
       if (++gb == 2) { gb = 0; g_phase ^= 1u; }
     }
+    cp_async_commit();
+    cp_async_wait<0>();
   }
   __syncthreads();
   if (warp == 4) {

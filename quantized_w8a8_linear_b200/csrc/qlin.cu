@@ -1573,7 +1573,7 @@ qlin_status qlin_layer_norm_backward(const void* dY, const void* X, qlin_dtype x
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int64_t kLoraMaxM = int64_t{1} << 28;
+constexpr int64_t kLoraMaxM = int64_t{1} << 28, kLoraMaxN = int64_t{1} << 28;
 constexpr int LORA_WG_MAX_CTAS = 160;
 
 // Adapter weights 16-bit [L, rows, cols]: box 64 columns x box_rows of one
@@ -1600,9 +1600,15 @@ struct LoraCall {
   LoraPlan view() const { return LoraPlan{plan, M, L}; }
 };
 
+struct LoraSplit {   // the backward pass's split rows
+  uint16_t* Hs = nullptr;
+  const float* G = nullptr;
+  uint16_t* Gs = nullptr;
+};
+
 // H [M,R] = scale * X W^T; X [M,C]. W_MN: W is B [L,C,R], else A [L,R,C].
 template <typename T, int RB, bool W_MN>
-qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H) {
+qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp) {
   CUtensorMap tw;
   if (W_MN) QLIN_TRY(make_tmap_adapters(&tw, W, c.L, C, c.R, LORA_SHRINK_BK));
   else QLIN_TRY(make_tmap_adapters(&tw, W, c.L, c.R, C, static_cast<int>(round_up(c.R, 16))));
@@ -1615,19 +1621,19 @@ qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, c
   const int64_t full = (c.M + LORA_TILE - 1) / LORA_TILE;
   int cluster = 8;
   while (cluster > 1 && (full * cluster > 2 * c.d->sms || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
-  LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), static_cast<const uint16_t*>(X), scale, H};
+  LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), static_cast<const uint16_t*>(X), scale, H, sp.Hs, sp.G, sp.Gs};
   return launch_dependent(kern, "k_lora_shrink launch", dim3(static_cast<unsigned>(lora_max_tiles(c.M, c.L) * cluster)), LORA_SHRINK_THREADS, smem, cluster, c.st, tw, p, cluster);
 }
 template <typename T, bool W_MN>
-qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H) {
-  return c.R <= 64 ? launch_lora_shrink_rb<T, 1, W_MN>(c, X, C, W, scale, H) : launch_lora_shrink_rb<T, 2, W_MN>(c, X, C, W, scale, H);
+qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp = {}) {
+  return c.R <= 64 ? launch_lora_shrink_rb<T, 1, W_MN>(c, X, C, W, scale, H, sp) : launch_lora_shrink_rb<T, 2, W_MN>(c, X, C, W, scale, H, sp);
 }
 
 // Y [M,N] += scale * H V^T. V_MN: V is A [L,R,N], else B [L,N,R].
 template <typename T, int RB, bool V_MN, bool VEC>
 qlin_status launch_lora_expand_rb(const LoraCall& c, const float* H, const void* V, int64_t N, const float* scale, void* Y) {
   CUtensorMap tv;
-  if (V_MN) QLIN_TRY(make_tmap_adapters(&tv, V, c.L, c.R, N, static_cast<int>(round_up(c.R, 16))));
+  if (V_MN) QLIN_TRY(make_tmap_adapters(&tv, V, c.L, c.R, N, RB * 64));
   else QLIN_TRY(make_tmap_adapters(&tv, V, c.L, N, c.R, LORA_EXPAND_BN));
   auto kern = k_lora_expand<T, RB, V_MN, VEC>;
   constexpr int smem = LoraExpandSmem<RB>::TOTAL;
@@ -1649,13 +1655,13 @@ qlin_status launch_lora_expand(const LoraCall& c, const float* H, const void* V,
 int lora_wg_ctas(const DeviceInfo* d) { return std::min(d->sms, LORA_WG_MAX_CTAS); }
 
 template <int RB>
-qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const float* dH, void* dA, const void* dY, int64_t N, const float* H,
+qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const uint16_t* dHs, void* dA, const void* dY, int64_t N, const uint16_t* Hs,
                               void* dB, float* part) {
   auto kern = k_lora_wgrad<RB>;
   constexpr int smem = LoraWgradSmem<RB>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dH, H}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
+  LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dHs, Hs}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
   QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", dim3(static_cast<unsigned>(p.ctas)), LORA_WG_THREADS, smem, 1, c.st, p));
   const int64_t segments = ((K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS) * c.L;
   const int64_t rg = c.R / 8;   // grid.y
@@ -1663,9 +1669,10 @@ qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const
                           LORA_WG_COLS, 0, 1, c.st, p);
 }
 
-qlin_status check_lora(int64_t M, int64_t L, int64_t R, const void* A, const void* B, const float* scale, const void* plan, size_t plan_bytes) {
+qlin_status check_lora(int64_t M, int64_t L, int64_t R, int64_t N, const void* A, const void* B, const float* scale, const void* plan, size_t plan_bytes) {
   if (L < 1 || L > LORA_MAX_L) return fail(QLIN_ERR_UNSUPPORTED, "L must be 1..%d adapters (got %lld)", LORA_MAX_L, static_cast<long long>(L));
   if (M > kLoraMaxM) return fail(QLIN_ERR_UNSUPPORTED, "M = %lld exceeds %lld", static_cast<long long>(M), static_cast<long long>(kLoraMaxM));
+  if (N > kLoraMaxN) return fail(QLIN_ERR_UNSUPPORTED, "N = %lld exceeds %lld", static_cast<long long>(N), static_cast<long long>(kLoraMaxN));
   if (R <= 0 || R % 8 != 0) return fail(QLIN_ERR_ALIGNMENT, "R must be a positive multiple of 8 (got %lld)", static_cast<long long>(R));
   if (R > LORA_MAX_R) return fail(QLIN_ERR_UNSUPPORTED, "R = %lld exceeds %d", static_cast<long long>(R), LORA_MAX_R);
   QLIN_REQ_PTR(A, "A");
@@ -1708,7 +1715,7 @@ qlin_status qlin_lora_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t 
                               int64_t R, int64_t N, const void* plan, size_t plan_bytes, float* H, void* Y, void* stream) {
   QLIN_TRY(check_common(X, xdt, M, K, N));
   if (M == 0 || N == 0) return ok();
-  QLIN_TRY(check_lora(M, L, R, A, B, scale, plan, plan_bytes));
+  QLIN_TRY(check_lora(M, L, R, N, A, B, scale, plan, plan_bytes));
   QLIN_REQ_PTR(H, "H");
   QLIN_REQ_PTR(Y, "Y");
   DeviceInfo* d;
@@ -1726,7 +1733,7 @@ qlin_status qlin_lora_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t 
 
 size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R) {
   if (M < 0 || R <= 0) return 0;
-  return static_cast<size_t>(round_up(4 * M * R, 256) + 4 * R * 2 * LORA_WG_COLS * LORA_WG_MAX_CTAS);
+  return static_cast<size_t>(3 * round_up(4 * M * R, 256) + 4 * R * 2 * LORA_WG_COLS * LORA_WG_MAX_CTAS);   // dH, its parts, H's parts, partial sums
 }
 
 qlin_status qlin_lora_backward(const void* dY, const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* A, const void* B,
@@ -1745,7 +1752,7 @@ qlin_status qlin_lora_backward(const void* dY, const void* X, qlin_dtype xdt, in
     QLIN_TRY(check_cuda(cudaMemsetAsync(dB, 0, static_cast<size_t>(2 * L * R * N), st), "cudaMemsetAsync"));
     return ok();
   }
-  QLIN_TRY(check_lora(M, L, R, A, B, scale, plan, plan_bytes));
+  QLIN_TRY(check_lora(M, L, R, N, A, B, scale, plan, plan_bytes));
   QLIN_REQ_PTR(dY, "dY");
   QLIN_REQ_PTR(H, "H");
   if (dX != nullptr && !aligned16(dX)) return fail(QLIN_ERR_ALIGNMENT, "dX is not 16-byte aligned");
@@ -1755,11 +1762,15 @@ qlin_status qlin_lora_backward(const void* dY, const void* X, qlin_dtype xdt, in
   DeviceInfo* d;
   QLIN_TRY(device_info(&d));
   const LoraCall c{M, L, R, static_cast<const int*>(plan), scale, d, st};
-  float* dH = static_cast<float*>(workspace);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round_up(4 * M * R, 256));
+  const int64_t rows_bytes = round_up(4 * M * R, 256);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* dH = reinterpret_cast<float*>(ws);
+  uint16_t* dHs = reinterpret_cast<uint16_t*>(ws + rows_bytes);
+  uint16_t* Hs = reinterpret_cast<uint16_t*>(ws + 2 * rows_bytes);
+  float* part = reinterpret_cast<float*>(ws + 3 * rows_bytes);
   using T = __nv_bfloat16;
-  QLIN_TRY((launch_lora_shrink<T, true>(c, dY, N, B, scale, dH)));
-  QLIN_TRY(R <= 64 ? launch_lora_wgrad<1>(c, X, K, dH, dA, dY, N, H, dB, part) : launch_lora_wgrad<2>(c, X, K, dH, dA, dY, N, H, dB, part));
+  QLIN_TRY((launch_lora_shrink<T, true>(c, dY, N, B, scale, dH, LoraSplit{dHs, H, Hs})));
+  QLIN_TRY(R <= 64 ? launch_lora_wgrad<1>(c, X, K, dHs, dA, dY, N, Hs, dB, part) : launch_lora_wgrad<2>(c, X, K, dHs, dA, dY, N, Hs, dB, part));
   if (dX != nullptr) QLIN_TRY((launch_lora_expand<T, true>(c, dH, A, K, nullptr, dX)));
   return ok();
 }
