@@ -898,9 +898,8 @@ struct LoraWgradUnits {
     units = static_cast<int64_t>(cgs) * tiles;
     ctas = static_cast<int>(units < p.ctas ? units : p.ctas);   // each has a unit: no slot is read that was not written
   }
-  // first unit of a CTA (of the CTAs past the last one with units: `units`), and the CTA of a unit
+  // first unit of a CTA (of the CTAs past the last one with units: `units`)
   __device__ __forceinline__ int64_t first(int64_t cta) const { return cta < ctas ? units * cta / ctas : units; }
-  __device__ __forceinline__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
 };
 
 template <int RB>
@@ -930,8 +929,14 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   uint64_t* drain_bar = tempty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr uint32_t ACC_COLS = 2 * RB * 64;
+  // R <= 64: one MMA multiplies both parts (N = 128: hi | lo, added by the
+  // epilogue), so that X's tile is read from shared memory once; two of N = 64
+  // took the MMA thread 65 us for 8191 rows against 50 us of HBM time
+  constexpr bool BOTH = RB == 1;
+  constexpr uint32_t G_COLS = BOTH ? 128 : RB * 64;   // accumulator columns of 128 columns of X
+  constexpr uint32_t ACC_COLS = 2 * G_COLS;
   constexpr uint32_t TCOLS = 2 * ACC_COLS;
+  static_assert(TCOLS <= 512, "TMEM");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1020,7 +1025,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   } else if (warp == 4) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idesc = idesc_f16(128, RB * 64, true) | IDESC_A_MN | IDESC_B_MN;
+      constexpr uint32_t idesc = idesc_f16(128, G_COLS, true) | IDESC_A_MN | IDESC_B_MN;
       int stage = 0, gb = 0, acc = 0;
       uint32_t phase = 0, g_phase = 0, acc_phase = 0;
       bool good = true, open = false;
@@ -1045,7 +1050,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
         if (!mbar_wait(&gfull_bar[gb], g_phase, abort_flag)) break;
         const uint32_t gs = smem_u32(sG(gb));
         for (int g = 0; good && g < 2 && c0 + g * 128 < (side ? p.cols[1] : p.cols[0]); ++g) {
-          const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g * RB * 64);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g) * G_COLS;
           if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { good = false; break; }
           fence_proxy_async_smem();   // X and G were written by cp.async, through the generic proxy
           tc_fence_after();
@@ -1054,10 +1059,10 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
           for (int h = 0; h < LORA_TILE / LORA_WG_ROWS; ++h) {
             if (LORA_WG_ROWS * h >= here.y) break;
             const uint64_t adesc = sdesc_mn128(smem_u32(sX(stage)) + h * (LORA_WG_ROWS * 128), LORA_TILE * 128);
-            const uint64_t bdesc = sdesc_mn128(gs + h * (LORA_WG_ROWS * 128), LORA_TILE * 128);
+            const uint64_t bdesc = sdesc_mn128(gs + h * (LORA_WG_ROWS * 128), BOTH ? S::G_BYTES : LORA_TILE * 128);
             const uint32_t more = open || h > 0 ? 1u : 0u;
 #pragma unroll
-            for (int k = 0; k < 2 * KS; ++k)   // both parts of G
+            for (int k = 0; k < (BOTH ? 1 : 2) * KS; ++k)   // the parts of G: side by side, or one after the other
               umma<2>(d, adesc + 128u * (k % KS), bdesc + 128u * (k % KS) + (k / KS) * (S::G_BYTES >> 4), idesc, k == 0 ? more : 1u);
           }
           umma_commit(&empty_bar[stage]);
@@ -1094,12 +1099,19 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (seg0 >= u0 ? 1 : 0)) * p.R * LORA_WG_COLS;
       for (int g = 0; g < 2 && c0 + g * 128 < C; ++g) {
         const int64_t col = c0 + g * 128 + q * 32 + lane;
-        const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g * RB * 64);
+        const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g) * G_COLS;
         for (int c = 0; c < p.R; c += 16) {
           uint32_t v[16];
           __syncwarp();
           tmem_ld16(at + static_cast<uint32_t>(c), v);
           tmem_wait16(v);
+          if constexpr (BOTH) {
+            uint32_t lo[16];
+            tmem_ld16(at + static_cast<uint32_t>(64 + c), lo);
+            tmem_wait16(lo);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(lo[i]));
+          }
 #pragma unroll
           for (int h = 0; h < 16; h += 8) {
             if (c + h < p.R && col < C) {
@@ -1185,47 +1197,46 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
 }
 
 // The segments k_lora_wgrad cut between CTAs, added in CTA order, and zeros
-// for adapters without rows. A CTA takes 8 values of R of a segment's 256 columns.
+// for adapters without rows. A CTA takes 8 values of R of 256 columns; blockIdx.x
+// names the boundary between two CTAs' ranges.
 __global__ void __launch_bounds__(LORA_WG_COLS) k_lora_wgrad_join(const LoraWgradParams p) {
   using T = __nv_bfloat16;
   griddep_wait();
   const LoraWgradUnits un(p);
-  const uint32_t L = static_cast<uint32_t>(p.plan.L);
-  const uint32_t segments = static_cast<uint32_t>(un.cgs) * L;
-  const bool any = un.tiles > 0;
-  for (uint32_t sg = blockIdx.x; sg < segments; sg += gridDim.x) {
-    const int a = static_cast<int>(sg % L), cg = static_cast<int>(sg / L);
+  const int r0 = static_cast<int>(blockIdx.y) * 8, c1 = static_cast<int>(blockIdx.x);
+  auto write = [&](int a, int cg, const float (&f)[8]) {
     const int side = cg >= un.cg0;
     const int64_t C = (side ? p.cols[1] : p.cols[0]), col = static_cast<int64_t>(cg - (side ? un.cg0 : 0)) * LORA_WG_COLS + threadIdx.x;
-    const int t0 = any ? p.plan.tile0()[a] : 0, t1 = any ? p.plan.tile0()[a + 1] : 0;
-    int c0 = 0, c1 = -1;   // CTAs that hold parts of the segment
-    int64_t s0 = 0;
-    if (t0 < t1) {
-      s0 = static_cast<int64_t>(cg) * un.tiles + t0;
-      c0 = un.owner(s0);
-      c1 = un.owner(s0 + (t1 - t0) - 1);
-      if (c0 == c1) continue;   // one CTA had it whole
+    if (col >= C) return;
+    if (side == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p.out[0][(static_cast<int64_t>(a) * p.R + r0 + i) * C + col] = from_f<T>(f[i]);
+    } else {
+      *reinterpret_cast<uint4*>(p.out[1] + (static_cast<int64_t>(a) * C + col) * p.R + r0) = narrow8<T>(f);
     }
-    if (col >= C) continue;
-    const float s = side ? __ldg(p.scale + a) : 1.0f;
-    for (int r0 = static_cast<int>(blockIdx.y) * 8; r0 < p.R; r0 += static_cast<int>(gridDim.y) * 8) {
+  };
+  // the segment that CTA c1 - 1 leaves to CTA c1, if it began in c1 - 1
+  if (c1 > 0 && c1 < un.ctas) {
+    const int64_t u = un.first(c1);
+    const int cg = static_cast<int>(u / un.tiles), t = static_cast<int>(u % un.tiles), a = p.plan.info(t).x;
+    const int64_t s0 = u - t + p.plan.tile0()[a], s1 = u - t + p.plan.tile0()[a + 1];
+    if (s0 < u && un.first(c1 - 1) <= s0) {
       float f[8] = {};
-      for (int c = c0; c <= c1; ++c) {
+      for (int c = c1 - 1; c < un.ctas && un.first(c) < s1; ++c) {
         const float* part = p.part + (static_cast<int64_t>(c) * 2 + (un.first(c) <= s0 ? 1 : 0)) * p.R * LORA_WG_COLS;
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] += part[(r0 + i) * LORA_WG_COLS + threadIdx.x];
       }
-      if (side == 0) {
+      const float s = cg >= un.cg0 ? __ldg(p.scale + a) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p.out[0][(static_cast<int64_t>(a) * p.R + r0 + i) * C + col] = from_f<T>(f[i]);
-      } else {
-        if (c1 >= c0) {   // else zeros, whatever the scale
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= s;
-        }
-        *reinterpret_cast<uint4*>(p.out[1] + (static_cast<int64_t>(a) * C + col) * p.R + r0) = narrow8<T>(f);
-      }
+      for (int i = 0; i < 8; ++i) f[i] *= s;
+      write(a, cg, f);
     }
+  }
+  const float zero[8] = {};
+  for (int a = 0; a < p.plan.L; ++a) {
+    if (un.tiles > 0 && p.plan.tile0()[a] < p.plan.tile0()[a + 1]) continue;
+    for (int cg = static_cast<int>(blockIdx.x); cg < un.cgs; cg += static_cast<int>(gridDim.x)) write(a, cg, zero);
   }
 }
 

@@ -1663,10 +1663,8 @@ qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const
   QLIN_TRY(allow_smem(kern, smem, set));
   LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dHs, Hs}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
   QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", dim3(static_cast<unsigned>(p.ctas)), LORA_WG_THREADS, smem, 1, c.st, p));
-  const int64_t segments = ((K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS) * c.L;
-  const int64_t rg = c.R / 8;   // grid.y
-  return launch_dependent(k_lora_wgrad_join, "k_lora_wgrad_join launch", dim3(static_cast<unsigned>(std::min<int64_t>(segments, 8 * c.d->sms)), static_cast<unsigned>(rg)),
-                          LORA_WG_COLS, 0, 1, c.st, p);
+  return launch_dependent(k_lora_wgrad_join, "k_lora_wgrad_join launch", dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(c.R / 8)), LORA_WG_COLS, 0, 1,
+                          c.st, p);
 }
 
 qlin_status check_lora(int64_t M, int64_t L, int64_t R, int64_t N, const void* A, const void* B, const float* scale, const void* plan, size_t plan_bytes) {
