@@ -16,6 +16,7 @@ Functions keep the C names:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -139,26 +140,42 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _tensor(t: Optional[torch.Tensor], name: str, shape, dtype, device):
-    """Pointer of an argument that the kernel reads or writes at this shape, dtype and device (None: NULL)."""
+def _tensor(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype, index: int):
+    """Pointer of an argument that the kernel reads or writes at this shape, dtype and CUDA device (None: NULL)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, X on {device}")
-    return _ptr(t)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _call(device, fn, *args) -> None:
+def _matrix(t: torch.Tensor, name: str = "X"):
+    """(pointer, dtype code, rows, columns, CUDA device index) of a 16-bit matrix."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    M, K = t.shape
+    if not t.is_cuda:
+        raise ValueError("libqlin takes CUDA tensors (device pointers)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), _dt(t), M, K, t.get_device()
+
+
+def _call(index: int, fn, *args) -> None:
     """The C call on the tensors' own device and on that device's current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)))
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)))
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != QLIN_OK:
+        _check(status)
 
 
 _ws_cache = {}
@@ -496,13 +513,11 @@ def qlin_layer_norm_forward(X: torch.Tensor, gamma: Optional[torch.Tensor] = Non
                             eps: float = 1e-6, Y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
                             rstd: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Layer norm of the rows of X [M,K]. mean, rstd: fp32 [M] to fill for the backward pass. Y may be X."""
-    M, K = X.shape
-    dev = X.device
-    x = _ptr(X)
+    x, dt, M, K, dev = _matrix(X)
     if Y is None:
         Y = torch.empty_like(X)
-    _call(dev, lib.qlin_layer_norm_forward, x, _dt(X), M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
-          _tensor(beta, "beta", (K,), X.dtype, dev), float(eps), _tensor(Y, "Y", (M, K), X.dtype, dev),
+    _call(dev, lib.qlin_layer_norm_forward, x, dt, M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
+          _tensor(beta, "beta", (K,), X.dtype, dev), eps, _tensor(Y, "Y", (M, K), X.dtype, dev),
           _tensor(mean, "mean", (M,), torch.float32, dev), _tensor(rstd, "rstd", (M,), torch.float32, dev))
     return Y
 
@@ -510,29 +525,25 @@ def qlin_layer_norm_forward(X: torch.Tensor, gamma: Optional[torch.Tensor] = Non
 def qlin_layer_norm_fp8_prep(X: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
                              eps: float = 1e-6, x_scale: Optional[torch.Tensor] = None):
     """Layer norm as FP8 codes (uint8 e4m3 [M,K]) and, in dynamic mode, per-token scales [M] for qlin_fp8_gemm."""
-    M, K = X.shape
-    dev = X.device
-    x = _ptr(X)
-    Xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
-    s_x = torch.empty((M,), dtype=torch.float32, device=dev) if x_scale is None else None
+    x, dt, M, K, dev = _matrix(X)
+    Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
+    s_x = torch.empty((M,), dtype=torch.float32, device=X.device) if x_scale is None else None
     if x_scale is not None:
         x_scale = x_scale.reshape(-1)
-    _call(dev, lib.qlin_layer_norm_fp8_prep, x, _dt(X), M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
-          _tensor(beta, "beta", (K,), X.dtype, dev), float(eps), _tensor(x_scale, "x_scale", (1,), torch.float32, dev),
-          _ptr(Xq), _ptr(s_x))
+    _call(dev, lib.qlin_layer_norm_fp8_prep, x, dt, M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
+          _tensor(beta, "beta", (K,), X.dtype, dev), eps, _tensor(x_scale, "x_scale", (1,), torch.float32, dev),
+          Xq.data_ptr(), None if s_x is None else s_x.data_ptr())
     return Xq, s_x
 
 
 def qlin_layer_norm_w4a8_prep(X: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
                               eps: float = 1e-6):
     """Layer norm as int8 codes [M,K] and per-token scales [M] for qlin_w4a8_gemm."""
-    M, K = X.shape
-    dev = X.device
-    x = _ptr(X)
-    Xq = torch.empty((M, K), dtype=torch.int8, device=dev)
-    s_x = torch.empty((M,), dtype=torch.float32, device=dev)
-    _call(dev, lib.qlin_layer_norm_w4a8_prep, x, _dt(X), M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
-          _tensor(beta, "beta", (K,), X.dtype, dev), float(eps), _ptr(Xq), _ptr(s_x))
+    x, dt, M, K, dev = _matrix(X)
+    Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    s_x = torch.empty((M,), dtype=torch.float32, device=X.device)
+    _call(dev, lib.qlin_layer_norm_w4a8_prep, x, dt, M, K, _tensor(gamma, "gamma", (K,), X.dtype, dev),
+          _tensor(beta, "beta", (K,), X.dtype, dev), eps, Xq.data_ptr(), s_x.data_ptr())
     return Xq, s_x
 
 
@@ -541,24 +552,38 @@ def qlin_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tens
                              dX: Optional[torch.Tensor] = None):
     """(dX, dgamma, dbeta) of qlin_layer_norm_forward; dgamma is None without gamma, and dbeta goes with it
     unless beta_grad says otherwise. dX may be dY or X."""
-    M, K = X.shape
-    dev = X.device
-    x = _ptr(X)
+    x, dt, M, K, dev = _matrix(X)
     if beta_grad is None:
         beta_grad = gamma is not None
     if dX is None:
         dX = torch.empty_like(X)
     dgamma = torch.empty_like(gamma) if gamma is not None else None
-    dbeta = torch.empty((K,), dtype=X.dtype, device=dev) if beta_grad else None
-    ws = None
+    dbeta = torch.empty((K,), dtype=X.dtype, device=X.device) if beta_grad else None
+    ws, n = None, 0
     if dgamma is not None or dbeta is not None:
-        n = int(lib.qlin_workspace_bytes(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K))
-        ws = torch.empty((max(n, 16),), dtype=torch.uint8, device=dev)
-    _call(dev, lib.qlin_layer_norm_backward, _tensor(dY, "dY", (M, K), X.dtype, dev), x, _dt(X), M, K,
+        n = max(_workspace_size(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K), 16)
+        ws = torch.empty((n,), dtype=torch.uint8, device=X.device)   # its own: calls on other streams have theirs
+    _call(dev, lib.qlin_layer_norm_backward, _tensor(dY, "dY", (M, K), X.dtype, dev), x, dt, M, K,
           _tensor(gamma, "gamma", (K,), X.dtype, dev), _tensor(mean, "mean", (M,), torch.float32, dev),
-          _tensor(rstd, "rstd", (M,), torch.float32, dev), _tensor(dX, "dX", (M, K), X.dtype, dev), _ptr(dgamma),
-          _ptr(dbeta), _ptr(ws), 0 if ws is None else ws.numel())
+          _tensor(rstd, "rstd", (M,), torch.float32, dev), _tensor(dX, "dX", (M, K), X.dtype, dev),
+          None if dgamma is None else dgamma.data_ptr(), None if dbeta is None else dbeta.data_ptr(),
+          None if ws is None else ws.data_ptr(), n)
     return dX, dgamma, dbeta
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(op: int, M: int, N: int, K: int) -> int:
+    return int(lib.qlin_workspace_bytes(op, M, N, K))
+
+
+@functools.lru_cache(maxsize=4096)
+def _plan_size(M: int, L: int) -> int:
+    return max(int(lib.qlin_lora_plan_bytes(M, L)), 16)
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_backward_size(M: int, R: int) -> int:
+    return max(int(lib.qlin_lora_backward_workspace_bytes(M, R)), 16)
 
 
 def qlin_lora_plan(idx: torch.Tensor, L: int) -> torch.Tensor:
@@ -568,34 +593,34 @@ def qlin_lora_plan(idx: torch.Tensor, L: int) -> torch.Tensor:
         raise TypeError("idx must be a 1-D int32 tensor")
     M, L = idx.shape[0], int(L)
     x = _ptr(idx)
-    n = int(lib.qlin_lora_plan_bytes(M, L))
-    plan = torch.empty((max(n, 16),), dtype=torch.uint8, device=idx.device)
-    _call(idx.device, lib.qlin_lora_plan, x, M, L, _ptr(plan), plan.numel())
+    plan = torch.empty((_plan_size(M, L),), dtype=torch.uint8, device=idx.device)
+    _call(idx.get_device(), lib.qlin_lora_plan, x, M, L, plan.data_ptr(), plan.numel())
     return plan
 
 
-def _lora_args(X, A, B, scale, plan):
-    M, K = X.shape
+def _lora_args(M, K, dtype, dev, A, B, scale, plan):
+    """(R, N, the C arguments from A to plan_bytes)"""
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [L, R, K] and B [L, N, R]")
-    L, R, N = A.shape[0], A.shape[1], B.shape[1]
-    dev = X.device
-    if plan.numel() != max(int(lib.qlin_lora_plan_bytes(M, L)), 16):
+    L, R, _ = A.shape
+    N = B.shape[1]
+    size = _plan_size(M, L)
+    if plan.numel() != size:
         raise ValueError(f"plan was not made for {M} rows and {L} adapters")
-    return M, K, L, R, N, dev, (_tensor(A, "A", (L, R, K), X.dtype, dev), _tensor(B, "B", (L, N, R), X.dtype, dev),
-                                _tensor(scale, "scale", (L,), torch.float32, dev), L, R, N,
-                                _tensor(plan, "plan", plan.shape, torch.uint8, dev), plan.numel())
+    return R, N, (_tensor(A, "A", (L, R, K), dtype, dev), _tensor(B, "B", (L, N, R), dtype, dev),
+                  _tensor(scale, "scale", (L,), torch.float32, dev), L, R, N,
+                  _tensor(plan, "plan", (size,), torch.uint8, dev), size)
 
 
 def qlin_lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, plan: torch.Tensor,
                       Y: torch.Tensor, H: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Adapters beside a projection, in place: Y[i] += scale[a] * (X[i] A[a]^T) B[a]^T for rows with an adapter.
     H: fp32 [M,R] to fill with X A^T for the backward pass (rows without an adapter are left as they were)."""
-    x = _ptr(X)
-    M, K, L, R, N, dev, args = _lora_args(X, A, B, scale, plan)
+    x, dt, M, K, dev = _matrix(X)
+    R, N, args = _lora_args(M, K, X.dtype, dev, A, B, scale, plan)
     if H is None:
-        H = torch.empty((M, R), dtype=torch.float32, device=dev)
-    _call(dev, lib.qlin_lora_forward, x, _dt(X), M, K, *args, _tensor(H, "H", (M, R), torch.float32, dev),
+        H = torch.empty((M, R), dtype=torch.float32, device=X.device)
+    _call(dev, lib.qlin_lora_forward, x, dt, M, K, *args, _tensor(H, "H", (M, R), torch.float32, dev),
           _tensor(Y, "Y", (M, N), X.dtype, dev))
     return Y
 
@@ -604,13 +629,14 @@ def qlin_lora_backward(dY: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: to
                        plan: torch.Tensor, H: torch.Tensor, dX: Optional[torch.Tensor] = None):
     """(dX, dA, dB) of qlin_lora_forward, bf16. dX: the projection's own input gradient, added to in place
     (None: not computed)."""
-    x = _ptr(X)
-    M, K, L, R, N, dev, args = _lora_args(X, A, B, scale, plan)
+    x, dt, M, K, dev = _matrix(X)
+    R, N, args = _lora_args(M, K, X.dtype, dev, A, B, scale, plan)
     dA, dB = torch.empty_like(A), torch.empty_like(B)
-    ws = torch.empty((max(int(lib.qlin_lora_backward_workspace_bytes(M, R)), 16),), dtype=torch.uint8, device=dev)
-    _call(dev, lib.qlin_lora_backward, _tensor(dY, "dY", (M, N), X.dtype, dev), x, _dt(X), M, K, *args,
-          _tensor(H, "H", (M, R), torch.float32, dev), _tensor(dX, "dX", (M, K), X.dtype, dev), _ptr(dA), _ptr(dB),
-          _ptr(ws), ws.numel())
+    n = _lora_backward_size(M, R)
+    ws = torch.empty((n,), dtype=torch.uint8, device=X.device)   # its own: calls on other streams have theirs
+    _call(dev, lib.qlin_lora_backward, _tensor(dY, "dY", (M, N), X.dtype, dev), x, dt, M, K, *args,
+          _tensor(H, "H", (M, R), torch.float32, dev), _tensor(dX, "dX", (M, K), X.dtype, dev), dA.data_ptr(),
+          dB.data_ptr(), ws.data_ptr(), n)
     return dX, dA, dB
 
 

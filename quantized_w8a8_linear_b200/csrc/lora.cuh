@@ -19,6 +19,8 @@
 //   k_lora_shrink  H or dH: contraction over K or N;
 //   k_lora_expand  Y or dX: contraction over R;
 //   k_lora_wgrad   dA and dB: contraction over the rows of an adapter.
+// A few rows (a decode step) go through k_lora_rows instead, one launch for
+// both products of up to eight rows of one adapter.
 //
 // H enters the second product as two 16-bit parts, hi = T(h) and
 // lo = T(h - hi), two MMAs on one staged operand: 16 (bf16) or 22 (fp16)
@@ -39,16 +41,22 @@ constexpr int LORA_MAX_L = 1024;
 
 // ---------------------------------------------------------------------------
 // plan: int32 words
-//   [0] M  [1] L  [2] tiles  [3..15] 0
+//   [0] M  [1] L  [2] tiles  [3] octets  [4..15] 0
 //   tile0 [L + 1]       first tile of each adapter (tile0[L] = tiles)
 //   info  [Tmax][2]     adapter and row count of a tile
 //   rows  [Tmax][128]   row numbers, in row order; M past the count
-// Tmax = M / 128 + min(L, M) bounds the sum of ceil(rows / 128) over adapters.
+//   octet [Omax][12]    adapter, row count, 0, 0, eight row numbers (M past the
+//                       count): the rows again in eights, up to LORA_OCTET_M rows
+// Tmax = M / 128 + min(L, M) bounds the sum of ceil(rows / 128) over adapters,
+// Omax = M / 8 + min(L, M) that of ceil(rows / 8).
 // ---------------------------------------------------------------------------
+constexpr int LORA_OCTET_M = 256, LORA_OCTET_WORDS = 12;
 __host__ __device__ inline int64_t lora_max_tiles(int64_t M, int64_t L) { return M / LORA_TILE + (L < M ? L : M); }
+__host__ __device__ inline int64_t lora_max_octets(int64_t M, int64_t L) { return M <= LORA_OCTET_M ? M / 8 + (L < M ? L : M) : 0; }
 __host__ __device__ inline int64_t lora_info_at(int64_t L) { return 16 + (L + 4) / 4 * 4; }
 __host__ __device__ inline int64_t lora_rows_at(int64_t M, int64_t L) { return lora_info_at(L) + (2 * lora_max_tiles(M, L) + 3) / 4 * 4; }
-__host__ __device__ inline int64_t lora_plan_words(int64_t M, int64_t L) { return lora_rows_at(M, L) + LORA_TILE * lora_max_tiles(M, L); }
+__host__ __device__ inline int64_t lora_octets_at(int64_t M, int64_t L) { return lora_rows_at(M, L) + LORA_TILE * lora_max_tiles(M, L); }
+__host__ __device__ inline int64_t lora_plan_words(int64_t M, int64_t L) { return lora_octets_at(M, L) + LORA_OCTET_WORDS * lora_max_octets(M, L); }
 
 struct LoraPlan {
   const int* w;
@@ -56,11 +64,13 @@ struct LoraPlan {
   __device__ __forceinline__ const int* tile0() const { return w + 16; }
   __device__ __forceinline__ int2 info(int t) const { return *reinterpret_cast<const int2*>(w + lora_info_at(L) + 2 * static_cast<int64_t>(t)); }
   __device__ __forceinline__ const int* rows(int t) const { return w + lora_rows_at(M, L) + static_cast<int64_t>(LORA_TILE) * t; }
-  // Tiles of the plan; 0, with QLIN_ERR_INVALID_ARG in the status word, when
+  __device__ __forceinline__ const int* octet(int o) const { return w + lora_octets_at(M, L) + static_cast<int64_t>(LORA_OCTET_WORDS) * o; }
+  // Tiles (octets) of the plan; 0, with QLIN_ERR_INVALID_ARG in the status word, when
   // the buffer holds another problem's plan (its row numbers are not used).
-  __device__ __forceinline__ int tiles() const {
+  __device__ __forceinline__ int tiles(bool octets = false) const {
     const int4 h = *reinterpret_cast<const int4*>(w);
-    if (h.x == static_cast<int>(M) && h.y == static_cast<int>(L) && h.z >= 0 && h.z <= lora_max_tiles(M, L)) return h.z;
+    if (h.x == static_cast<int>(M) && h.y == static_cast<int>(L) && h.z >= 0 && h.z <= lora_max_tiles(M, L) && h.w >= 0 && h.w <= lora_max_octets(M, L))
+      return octets ? h.w : h.z;
     atomicExch(&g_status, 1 /* QLIN_ERR_INVALID_ARG */);
     return 0;
   }
@@ -74,8 +84,8 @@ constexpr int LORA_PLAN_THREADS = 1024;
 // row's place within 32 rows from the ballot of its equals. No atomics, so
 // the order (and every sum over it) is the same in every run.
 __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx, int64_t M, int64_t L64, int* plan) {
-  extern __shared__ int lora_count[];   // [32][L]
-  __shared__ int warp_total[32];
+  extern __shared__ int lora_count[];   // [32][L], then [L] first octets
+  __shared__ int warp_total[32], warp_octets[32];
   const int L = static_cast<int>(L64);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t per = (M + 1023) / 1024 * 32;
@@ -107,17 +117,30 @@ __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx,
     }
   }
   const int tiles = (n + LORA_TILE - 1) / LORA_TILE;
-  int scan = tiles;
+  const bool in_octets = M <= LORA_OCTET_M;
+  const int octets = in_octets ? (n + 7) / 8 : 0;
+  int scan = tiles, oscan = octets;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += u;
+    const int u = __shfl_up_sync(0xffffffffu, scan, o), v = __shfl_up_sync(0xffffffffu, oscan, o);
+    if (lane >= o) {
+      scan += u;
+      oscan += v;
+    }
   }
-  if (lane == 31) warp_total[warp] = scan;
+  if (lane == 31) {
+    warp_total[warp] = scan;
+    warp_octets[warp] = oscan;
+  }
   __syncthreads();
-  int before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_total[w];
-  const int first = before + scan - tiles;
+  int before = 0, obefore = 0;
+  for (int w = 0; w < warp; ++w) {
+    before += warp_total[w];
+    obefore += warp_octets[w];
+  }
+  const int first = before + scan - tiles, ofirst = obefore + oscan - octets;
+  int* first_octet = lora_count + 32 * L;
+  int* octet = plan + lora_octets_at(M, L);
   if (tid < L) {
     tile0[tid] = first;
     if (tid == L - 1) tile0[L] = first + tiles;
@@ -127,18 +150,33 @@ __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx,
     }
     for (int i = n; i < tiles * LORA_TILE; ++i) rows[static_cast<int64_t>(first) * LORA_TILE + i] = static_cast<int>(M);
     for (int w = 0; w < 32; ++w) lora_count[w * L + tid] += first * LORA_TILE;
+    first_octet[tid] = ofirst - first * (LORA_TILE / 8);   // of the place lora_count gives a row
+    for (int t = 0; t < octets; ++t) {
+      int* o = octet + LORA_OCTET_WORDS * (ofirst + t);
+      o[0] = tid;
+      o[1] = n - 8 * t < 8 ? n - 8 * t : 8;
+      o[2] = o[3] = 0;
+      for (int i = n - 8 * t; i < 8; ++i) o[4 + i] = static_cast<int>(M);
+    }
   }
   if (tid < 16) {
-    int total = 0;
-    for (int w = 0; w < 32; ++w) total += warp_total[w];
-    plan[tid] = tid == 0 ? static_cast<int>(M) : tid == 1 ? L : tid == 2 ? total : 0;
+    int total = 0, ototal = 0;
+    for (int w = 0; w < 32; ++w) {
+      total += warp_total[w];
+      ototal += warp_octets[w];
+    }
+    plan[tid] = tid == 0 ? static_cast<int>(M) : tid == 1 ? L : tid == 2 ? total : tid == 3 ? ototal : 0;
   }
   __syncthreads();
   for (int64_t m0 = lo; m0 < hi; m0 += 32) {
     const int a = adapter(m0 + lane);
     const uint32_t same = __match_any_sync(0xffffffffu, a);
     const int rank = __popc(same & ((1u << lane) - 1u));
-    if (a >= 0) rows[mine[a] + rank] = static_cast<int>(m0 + lane);
+    if (a >= 0) {
+      const int at = mine[a] + rank;
+      rows[at] = static_cast<int>(m0 + lane);
+      if (in_octets) octet[LORA_OCTET_WORDS * (first_octet[a] + at / 8) + 4 + at % 8] = static_cast<int>(m0 + lane);
+    }
     __syncwarp();
     if (a >= 0 && rank == 0) mine[a] += __popc(same);
     __syncwarp();
@@ -255,6 +293,153 @@ __device__ __forceinline__ void store_split4(uint16_t* row, int R, const float4&
   split8<T>(f, hi, lo);
   *reinterpret_cast<uint2*>(row) = make_uint2(hi.x, hi.y);
   *reinterpret_cast<uint2*>(row + R) = make_uint2(lo.x, lo.y);
+}
+
+// ---------------------------------------------------------------------------
+// k_lora_rows: both products of up to eight rows of one adapter, for batches
+// of a few rows. A cluster of eight CTAs takes an octet: each CTA forms H over
+// an eighth of K (a warp a row of A, all eight rows of X at once, so A is read
+// once), the partial sums meet through distributed shared memory in rank
+// order, and each CTA updates an eighth of the columns of Y, a thread a
+// column. Latency is all that counts here (64 rows of 32 adapters of rank 16
+// move 20 MB, 3 us of HBM time): the CTAs ask for their part of B and Y into
+// L2 before they turn to A, and there is no second launch. fp32 FMAs: at these
+// sizes the tensor cores would wait for the same bytes.
+// ---------------------------------------------------------------------------
+constexpr int LORA_ROWS_THREADS = 256, LORA_ROWS_CLUSTER = 8;
+
+struct LoraRowsParams {
+  LoraPlan plan;
+  int64_t K, N;
+  int R;
+  const uint16_t* X;    // [M,K]
+  const uint16_t* A;    // [L,R,K]
+  const uint16_t* B;    // [L,N,R]
+  const float* scale;   // [L]
+  float* H;             // [M,R]
+  uint16_t* Y;          // [M,N]
+};
+
+// bytes: the eight rows' part of X (16-bit), partial sums and sums of H
+inline int lora_rows_smem(int64_t K, int64_t R) {
+  const int64_t kv = (K / 8 + LORA_ROWS_CLUSTER - 1) / LORA_ROWS_CLUSTER;
+  return static_cast<int>(8 * kv * 16 + 2 * 8 * R * 4);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p))); }
+
+template <typename T>
+__global__ void __launch_bounds__(LORA_ROWS_THREADS, 2) k_lora_rows(const LoraRowsParams p) {
+  extern __shared__ uint4 lora_x[];   // [8][kvs] chunks of X, part [8][R], sum [8][R]
+  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank()), R = p.R;
+  griddep_wait();
+  const int o = blockIdx.x / LORA_ROWS_CLUSTER;
+  if (o >= p.plan.tiles(true)) return;   // all CTAs of the cluster
+  const int* oct = p.plan.octet(o);
+  const int a = oct[0], n = oct[1];
+  const int KV = static_cast<int>(p.K / 8), kvs = (KV + LORA_ROWS_CLUSTER - 1) / LORA_ROWS_CLUSTER;
+  const int k0 = KV * rank / LORA_ROWS_CLUSTER, kn = KV * (rank + 1) / LORA_ROWS_CLUSTER - k0;
+  const int n0 = static_cast<int>(p.N * rank / LORA_ROWS_CLUSTER), n1 = static_cast<int>(p.N * (rank + 1) / LORA_ROWS_CLUSTER);
+  const uint16_t* A = p.A + static_cast<int64_t>(a) * R * p.K + 8 * k0;
+  const uint16_t* B = p.B + static_cast<int64_t>(a) * p.N * R;
+  float* part = reinterpret_cast<float*>(lora_x + 8 * kvs);
+  float* sum = part + 8 * R;
+
+  for (int e = tid; e < n * kn; e += LORA_ROWS_THREADS) {
+    const int j = e / kn, c = e % kn;
+    cp_async16(&lora_x[j * kvs + c], p.X + oct[4 + j] * p.K + 8 * (k0 + c), true);
+  }
+  cp_async_commit();
+  for (int64_t b = 128 * tid; b < 2 * static_cast<int64_t>(n1 - n0) * R; b += 128 * LORA_ROWS_THREADS)
+    prefetch_l2(reinterpret_cast<const uint8_t*>(B + static_cast<int64_t>(n0) * R) + b);
+  for (int j = warp; j < n; j += LORA_ROWS_THREADS / 32)
+    for (int b = 128 * lane; b < 2 * (n1 - n0); b += 128 * 32) prefetch_l2(reinterpret_cast<const uint8_t*>(p.Y + oct[4 + j] * p.N + n0) + b);
+  cp_async_wait<0>();
+  __syncthreads();
+
+  // H over this CTA's part of K: rows r, r + 8 of A a warp (r < R; R % 8 == 0, the second one may be absent)
+  for (int r = warp; r < R; r += 16) {
+    const bool two = r + 8 < R;
+    const uint4* a0 = reinterpret_cast<const uint4*>(A + static_cast<int64_t>(r) * p.K);
+    const uint4* a1 = reinterpret_cast<const uint4*>(A + static_cast<int64_t>(two ? r + 8 : r) * p.K);
+    float h[2][8] = {};
+#pragma unroll 2
+    for (int c = lane; c < kn; c += 32) {
+      const uint4 v0 = ld_nc_v4(a0 + c), v1 = ld_nc_v4(a1 + c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < n) {
+          const uint4 x = lora_x[j * kvs + c];
+          h[0][j] = fma2_mixed<bf>(x.w, v0.w, fma2_mixed<bf>(x.z, v0.z, fma2_mixed<bf>(x.y, v0.y, fma2_mixed<bf>(x.x, v0.x, h[0][j]))));
+          h[1][j] = fma2_mixed<bf>(x.w, v1.w, fma2_mixed<bf>(x.z, v1.z, fma2_mixed<bf>(x.y, v1.y, fma2_mixed<bf>(x.x, v1.x, h[1][j]))));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = warp_sum(h[i][j]);
+        if (lane == 0 && (i == 0 || two)) part[j * R + r + 8 * i] = t;
+      }
+  }
+  cluster_sync();
+  for (int e = 4 * tid; e < 8 * R; e += 4 * LORA_ROWS_THREADS) {
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < LORA_ROWS_CLUSTER; ++k) {
+      const float4 f = ld_cluster_f4(smem_u32(part + e), static_cast<uint32_t>(k));
+      t = make_float4(t.x + f.x, t.y + f.y, t.z + f.z, t.w + f.w);
+    }
+    *reinterpret_cast<float4*>(sum + e) = t;
+    const int j = e / R;
+    if (rank == 0 && j < n) *reinterpret_cast<float4*>(p.H + static_cast<int64_t>(oct[4 + j]) * R + e % R) = t;
+  }
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // this CTA has read its peers' partial sums
+  __syncthreads();
+  const float s = __ldg(p.scale + a);
+  uint16_t* yr[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) yr[j] = p.Y + (j < n ? oct[4 + j] * p.N : 0);
+  for (int col = n0 + tid; col < n1; col += 2 * LORA_ROWS_THREADS) {   // columns col and col + 256
+    const bool two = col + LORA_ROWS_THREADS < n1;
+    const int next = two ? col + LORA_ROWS_THREADS : col;
+    uint16_t y0[8], y1[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < n) {
+        y0[j] = yr[j][col];
+        y1[j] = yr[j][next];
+      }
+    }
+    float d0[8] = {}, d1[8] = {};
+    const uint4* b0 = reinterpret_cast<const uint4*>(B + static_cast<int64_t>(col) * R);
+    const uint4* b1 = reinterpret_cast<const uint4*>(B + static_cast<int64_t>(next) * R);
+    for (int c = 0; c < R / 8; ++c) {
+      float f[8], g[8];
+      widen8<T>(__ldg(b0 + c), f);
+      widen8<T>(__ldg(b1 + c), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < n) {
+          const float4 u = *reinterpret_cast<const float4*>(sum + j * R + 8 * c), v = *reinterpret_cast<const float4*>(sum + j * R + 8 * c + 4);
+          d0[j] = fmaf(f[3], u.w, fmaf(f[2], u.z, fmaf(f[1], u.y, fmaf(f[0], u.x, d0[j]))));
+          d1[j] = fmaf(g[3], u.w, fmaf(g[2], u.z, fmaf(g[1], u.y, fmaf(g[0], u.x, d1[j]))));
+          d0[j] = fmaf(f[7], v.w, fmaf(f[6], v.z, fmaf(f[5], v.y, fmaf(f[4], v.x, d0[j]))));
+          d1[j] = fmaf(g[7], v.w, fmaf(g[6], v.z, fmaf(g[5], v.y, fmaf(g[4], v.x, d1[j]))));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < n) {
+        yr[j][col] = from_f<T>(fmaf(d0[j], s, to_f<T>(y0[j])));
+        if (two) yr[j][next] = from_f<T>(fmaf(d1[j], s, to_f<T>(y1[j])));
+      }
+    }
+  }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");     // no CTA leaves while another reads its partial sums
 }
 
 // ---------------------------------------------------------------------------

@@ -35,12 +35,6 @@ struct NormArgs {
   const float* x_scale;    // [1] static scale
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // Sum (or maximum) over the CTA, the same value in every thread and in a
 // fixed order. Consecutive calls alternate between two rows of `red`, so one
 // barrier a call is enough: a row is written again only after every thread

@@ -1576,6 +1576,12 @@ namespace {
 constexpr int64_t kLoraMaxM = int64_t{1} << 28, kLoraMaxN = int64_t{1} << 28;
 constexpr int LORA_WG_MAX_CTAS = 160;
 
+// Which kernels take the forward pass. Measured at K = N = 4096, bf16, one
+// adapter and 32, us, k_lora_rows against the two tile kernels:
+//   R 16: M 64 7.0, 7.3 : 11.0, 18.9   M 256 8.4, 13.8 : 11.7, 20.4
+//   R 64: M 16 15.5, 12.5 : 10.6, 15.9   M 64 15.6, 18.0 : 11.4, 19.3
+bool lora_by_rows(int64_t M, int64_t R) { return M <= LORA_OCTET_M && R <= 32 && M * R <= 4096; }
+
 // Adapter weights 16-bit [L, rows, cols]: box 64 columns x box_rows of one
 // adapter, 128B swizzle; rows past `rows` read as zeros, not as the next adapter's.
 qlin_status make_tmap_adapters(CUtensorMap* m, const void* base, int64_t L, int64_t rows, int64_t cols, int box_rows) {
@@ -1652,6 +1658,18 @@ qlin_status launch_lora_expand(const LoraCall& c, const float* H, const void* V,
   else return c.R <= 64 ? launch_lora_expand_rb<T, 1, V_MN, false>(c, H, V, N, scale, Y) : launch_lora_expand_rb<T, 2, V_MN, false>(c, H, V, N, scale, Y);
 }
 
+// Both products of a few rows in one launch.
+template <typename T>
+qlin_status launch_lora_rows(const LoraCall& c, const void* X, int64_t K, const void* A, const void* B, int64_t N, float* H, void* Y) {
+  auto kern = k_lora_rows<T>;
+  static std::atomic<bool> set[16] = {};
+  QLIN_TRY(allow_smem(kern, lora_rows_smem(kMaxK, LORA_MAX_R), set));
+  LoraRowsParams p{c.view(), K, N, static_cast<int>(c.R), static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B),
+                   c.scale, H, static_cast<uint16_t*>(Y)};
+  return launch_dependent(kern, "k_lora_rows launch", dim3(static_cast<unsigned>(lora_max_octets(c.M, c.L) * LORA_ROWS_CLUSTER)), LORA_ROWS_THREADS,
+                          lora_rows_smem(K, c.R), LORA_ROWS_CLUSTER, c.st, p);
+}
+
 int lora_wg_ctas(const DeviceInfo* d) { return std::min(d->sms, LORA_WG_MAX_CTAS); }
 
 template <int RB>
@@ -1703,8 +1721,8 @@ qlin_status qlin_lora_plan(const int32_t* idx, int64_t M, int64_t L, void* plan,
   DeviceInfo* d;
   QLIN_TRY(device_info(&d));
   static std::atomic<bool> set[16] = {};
-  QLIN_TRY(allow_smem(k_lora_plan, 32 * LORA_MAX_L * 4, set));
-  k_lora_plan<<<1, LORA_PLAN_THREADS, static_cast<size_t>(32 * L * 4), static_cast<cudaStream_t>(stream)>>>(idx, M, L, static_cast<int*>(plan));
+  QLIN_TRY(allow_smem(k_lora_plan, 33 * LORA_MAX_L * 4, set));
+  k_lora_plan<<<1, LORA_PLAN_THREADS, static_cast<size_t>(33 * L * 4), static_cast<cudaStream_t>(stream)>>>(idx, M, L, static_cast<int*>(plan));
   QLIN_TRY(check_cuda(cudaGetLastError(), "k_lora_plan launch"));
   return ok();
 }
@@ -1719,7 +1737,9 @@ qlin_status qlin_lora_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t 
   DeviceInfo* d;
   QLIN_TRY(device_info(&d));
   const LoraCall c{M, L, R, static_cast<const int*>(plan), scale, d, static_cast<cudaStream_t>(stream)};
-  if (xdt == QLIN_BF16) {
+  if (lora_by_rows(M, R)) {
+    QLIN_TRY(xdt == QLIN_BF16 ? launch_lora_rows<__nv_bfloat16>(c, X, K, A, B, N, H, Y) : launch_lora_rows<__half>(c, X, K, A, B, N, H, Y));
+  } else if (xdt == QLIN_BF16) {
     QLIN_TRY((launch_lora_shrink<__nv_bfloat16, false>(c, X, K, A, nullptr, H)));
     QLIN_TRY((launch_lora_expand<__nv_bfloat16, false>(c, H, B, N, scale, Y)));
   } else {
