@@ -57,14 +57,37 @@ __device__ __forceinline__ float cta_reduce(float v, float (*red)[16], int& slot
   return t;
 }
 
+// 8 16-bit values -> four fp32 pairs: the passes below work on pairs, two IEEE
+// operations an instruction (a row of 4096 took 15 instructions an element one
+// by one, half of the kernel's time at 4.6 TB/s).
+typedef unsigned long long f32x2;
+template <typename T>
+__device__ __forceinline__ void widen8x2(const uint4& u, f32x2 (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      f[i] = f32x2_of(w[i] << 16, w[i] & 0xFFFF0000u);
+    } else {
+      f[i] = f32x2_of(__float_as_uint(to_f<T>(static_cast<uint16_t>(w[i]))), __float_as_uint(to_f<T>(static_cast<uint16_t>(w[i] >> 16))));
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 narrow8x2(const f32x2 (&f)[4]) {
+  return make_uint4(narrow2<T>(lo_f(f[0]), hi_f(f[0])), narrow2<T>(lo_f(f[1]), hi_f(f[1])), narrow2<T>(lo_f(f[2]), hi_f(f[2])),
+                    narrow2<T>(lo_f(f[3]), hi_f(f[3])));
+}
+__device__ __forceinline__ f32x2 twice(float v) { return f32x2_of(__float_as_uint(v), __float_as_uint(v)); }
+
 // One row at a time per CTA, V 16-byte vectors of it per thread; the CTAs
-// stride over the rows. gamma and beta stay in registers when a thread holds
-// at most four vectors of them.
+// stride over the rows. gamma and beta stay in registers (widened up to two
+// vectors a thread, as they are up to four).
 template <typename T, int V, int OUT>
 __global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_fwd(const NormArgs a) {
   extern __shared__ uint4 norm_ring[];   // [NORM_STAGES][V][threads]
   __shared__ float red[2][16];
-  constexpr bool HOLD = V <= 4;
+  constexpr bool WIDE = V <= 2, HOLD = V <= 4;
   const int nt = blockDim.x, tid = threadIdx.x;
   const int KV = static_cast<int>(a.K / 8);
   const int64_t step = gridDim.x;
@@ -82,14 +105,18 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_fwd(const NormArgs a)
   };
   auto affine = [&](const uint16_t* p, int j, float none) {
     const int v = j * nt + tid;
-    const uint32_t n2 = pack2<T>(none, none);
+    const uint32_t n2 = narrow2<T>(none, none);
     return p != nullptr && v < KV ? *reinterpret_cast<const uint4*>(p + 8 * v) : make_uint4(n2, n2, n2, n2);
   };
   for (int i = 0; i < NORM_STAGES - 1; ++i) fetch(blockIdx.x + i * step, i);
-  uint4 g[HOLD ? V : 1], b[HOLD ? V : 1];
-  if constexpr (HOLD) {
+  uint4 g[HOLD && !WIDE ? V : 1], b[HOLD && !WIDE ? V : 1];
+  f32x2 gw[WIDE ? V : 1][4], bw[WIDE ? V : 1][4];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+  for (int j = 0; j < V; ++j) {
+    if constexpr (WIDE) {
+      widen8x2<T>(affine(a.gamma, j, 1.0f), gw[j]);
+      widen8x2<T>(affine(a.beta, j, 0.0f), bw[j]);
+    } else if constexpr (HOLD) {
       g[j] = affine(a.gamma, j, 1.0f);
       b[j] = affine(a.beta, j, 0.0f);
     }
@@ -102,47 +129,48 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_fwd(const NormArgs a)
   for (int64_t row = blockIdx.x; row < a.M; row += step) {
     fetch(row + (NORM_STAGES - 1) * step, st == 0 ? NORM_STAGES - 1 : st - 1);
     cp_async_wait<NORM_STAGES - 1>();
-    uint4 x[V];
-    float s = 0.0f;
+    f32x2 x[V][4];   // the row, then its differences from the mean
+    f32x2 s2 = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      x[j] = j * nt + tid < KV ? norm_ring[(st * V + j) * nt + tid] : make_uint4(0, 0, 0, 0);
-      float f[8];
-      widen8<T>(x[j], f);
-      s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      widen8x2<T>(j * nt + tid < KV ? norm_ring[(st * V + j) * nt + tid] : make_uint4(0, 0, 0, 0), x[j]);
+      s2 = add_f32x2(s2, add_f32x2(add_f32x2(x[j][0], x[j][1]), add_f32x2(x[j][2], x[j][3])));
     }
-    const float mean = cta_reduce<false>(s, red, slot) * rK;
-    float q = 0.0f;
+    const float mean = cta_reduce<false>(lo_f(s2) + hi_f(s2), red, slot) * rK;
+    const f32x2 minus = twice(-mean);
+    f32x2 q2 = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float f[8];
-      widen8<T>(x[j], f);
-      float d = 0.0f;
+      f32x2 d = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d = fmaf(f[i] - mean, f[i] - mean, d);
-      if (j * nt + tid < KV) q += d;
+      for (int i = 0; i < 4; ++i) {
+        x[j][i] = add_f32x2(x[j][i], minus);
+        d = fma_f32x2(x[j][i], x[j][i], d);
+      }
+      if (j * nt + tid < KV) q2 = add_f32x2(q2, d);
     }
-    const float var = cta_reduce<false>(q, red, slot) * rK;
+    const float var = cta_reduce<false>(lo_f(q2) + hi_f(q2), red, slot) * rK;
     const float rstd = 1.0f / sqrtf(var + a.eps);
     if (tid == 0) {
       if (a.mean != nullptr) a.mean[row] = mean;
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
-    auto value = [&](int j, float (&f)[8]) {
-      widen8<T>(x[j], f);
-      float gf[8], bf[8];
-      widen8<T>(HOLD ? g[HOLD ? j : 0] : affine(a.gamma, j, 1.0f), gf);
-      widen8<T>(HOLD ? b[HOLD ? j : 0] : affine(a.beta, j, 0.0f), bf);
+    const f32x2 r2 = twice(rstd);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = fmaf((f[i] - mean) * rstd, gf[i], bf[i]);
-    };
+    for (int j = 0; j < V; ++j) {
+      f32x2 gj[4], bj[4];
+      if constexpr (!WIDE) {
+        widen8x2<T>(HOLD ? g[HOLD ? j : 0] : affine(a.gamma, j, 1.0f), gj);
+        widen8x2<T>(HOLD ? b[HOLD ? j : 0] : affine(a.beta, j, 0.0f), bj);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[j][i] = fma_f32x2(mul_f32x2(x[j][i], r2), WIDE ? gw[WIDE ? j : 0][i] : gj[i], WIDE ? bw[WIDE ? j : 0][i] : bj[i]);
+    }
     if constexpr (OUT == NORM_OUT_16) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int v = j * nt + tid;
-        float f[8];
-        value(j, f);
-        if (v < KV) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.Y) + row * a.K + 8 * static_cast<int64_t>(v)) = narrow8<T>(f);
+        if (v < KV) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.Y) + row * a.K + 8 * static_cast<int64_t>(v)) = narrow8x2<T>(x[j]);
       }
     } else {
       float inv = inv_static;
@@ -150,32 +178,29 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_fwd(const NormArgs a)
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          float f[8];
-          value(j, f);
           if (j * nt + tid < KV) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(lo_f(x[j][i])), fabsf(hi_f(x[j][i]))));
           }
         }
         const float sx = cta_reduce<true>(m, red, slot) / (OUT == NORM_OUT_INT8 ? 127.0f : 448.0f);
         inv = 1.0f / sx;
         if (tid == 0) a.s_x[row] = sx;
       }
+      inv = fminf(inv, 3.402823466e38f);   // a zero stays zero where 1 / s overflows; all else saturates either way
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int v = j * nt + tid;
-        float f[8];
-        value(j, f);
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const f32x2 u = x[j][2 * h], t = x[j][2 * h + 1];
           if constexpr (OUT == NORM_OUT_INT8) {
-            w[h] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[h] |= static_cast<uint32_t>(q_int(f[4 * h + i], inv, 127) & 0xFF) << (8 * i);
+            w[h] = static_cast<uint32_t>(q_int(lo_f(u), inv, 127) & 0xFF) | static_cast<uint32_t>(q_int(hi_f(u), inv, 127) & 0xFF) << 8 |
+                   static_cast<uint32_t>(q_int(lo_f(t), inv, 127) & 0xFF) << 16 | static_cast<uint32_t>(q_int(hi_f(t), inv, 127) & 0xFF) << 24;
           } else {
-            w[h] = e4m3x2(q_e4m3_in(f[4 * h], inv), q_e4m3_in(f[4 * h + 1], inv)) |
-                   e4m3x2(q_e4m3_in(f[4 * h + 2], inv), q_e4m3_in(f[4 * h + 3], inv)) << 16;
+            const f32x2 y0 = mul_f32x2(u, twice(inv)), y1 = mul_f32x2(t, twice(inv));
+            w[h] = e4m3x2(lo_f(y0), hi_f(y0)) | e4m3x2(lo_f(y1), hi_f(y1)) << 16;
           }
         }
         if (v < KV)
@@ -202,10 +227,13 @@ struct NormBwdArgs {
 // sum d * xh are reduced behind one barrier. Each thread keeps the column
 // sums of its own 8 V columns in registers over all rows of its CTA and
 // writes them once at the end, for k_norm_bwd_cols to add in CTA order.
-template <typename T, int V, bool COLS>
-__global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_bwd(const NormBwdArgs a) {
+// MAXT: the threads of a row at most (256 or 512); 512 of them an SM, so that
+// the compiler may spread a row's independent work over 128 registers (left to
+// itself, at 110, 16640 rows of 4096 took 87 us instead of 70).
+template <typename T, int V, bool COLS, int MAXT>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs a) {
   extern __shared__ uint4 norm_ring[];   // [NORM_STAGES][2 V][threads]: x, dy
-  __shared__ float2 red[2][16];
+  __shared__ float red[2][2][16];
   const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = nt >> 5;
   const int KV = static_cast<int>(a.K / 8);
   const int64_t step = gridDim.x;
@@ -222,70 +250,96 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_bwd(const NormBwdArgs
     cp_async_commit();
   };
   for (int i = 0; i < NORM_STAGES - 1; ++i) fetch(blockIdx.x + i * step, i);
-  uint4 g[V];
+  // up to two vectors a thread: gamma widened, and a row's xh and d kept from
+  // the sums to the output; beyond that both are formed again from the ring
+  constexpr bool HOLD = V <= 2;
+  uint4 g[HOLD ? 1 : V];
+  f32x2 gw[HOLD ? V : 1][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int v = j * nt + tid;
-    const uint32_t one = pack2<T>(1.0f, 1.0f);
-    g[j] = a.gamma != nullptr && v < KV ? *reinterpret_cast<const uint4*>(a.gamma + 8 * v) : make_uint4(one, one, one, one);
+    const uint32_t o = narrow2<T>(1.0f, 1.0f);
+    const uint4 u = a.gamma != nullptr && v < KV ? *reinterpret_cast<const uint4*>(a.gamma + 8 * v) : make_uint4(o, o, o, o);
+    if constexpr (HOLD) widen8x2<T>(u, gw[j]);
+    else g[j] = u;
   }
-  float dg[COLS ? 8 * V : 1] = {}, db[COLS ? 8 * V : 1] = {};
+  f32x2 dg[COLS ? V : 1][4] = {}, db[COLS ? V : 1][4] = {};
   const float rK = 1.0f / static_cast<float>(a.K);
   int st = 0, slot = 0;
+  // xh and d of vector j; dy on the way
+  auto terms = [&](int j, const f32x2& minus, const f32x2& r2, f32x2 (&xh)[4], f32x2 (&d)[4], f32x2 (&dy)[4]) {
+    widen8x2<T>(norm_ring[(st * 2 * V + j) * nt + tid], xh);
+    widen8x2<T>(norm_ring[(st * 2 * V + V + j) * nt + tid], dy);
+    f32x2 gj[4];
+    if constexpr (!HOLD) widen8x2<T>(g[HOLD ? 0 : j], gj);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      xh[i] = mul_f32x2(add_f32x2(xh[i], minus), r2);
+      d[i] = mul_f32x2(dy[i], HOLD ? gw[HOLD ? j : 0][i] : gj[i]);
+    }
+  };
+  float next_mean = 0.0f, next_rstd = 0.0f;   // looked up a row ahead
+  if (blockIdx.x < a.M) {
+    next_mean = __ldg(a.mean + blockIdx.x);
+    next_rstd = __ldg(a.rstd + blockIdx.x);
+  }
   for (int64_t row = blockIdx.x; row < a.M; row += step) {
-    const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
+    const float mean = next_mean, rstd = next_rstd;
+    if (row + step < a.M) {
+      next_mean = __ldg(a.mean + row + step);
+      next_rstd = __ldg(a.rstd + row + step);
+    }
     fetch(row + (NORM_STAGES - 1) * step, st == 0 ? NORM_STAGES - 1 : st - 1);
     cp_async_wait<NORM_STAGES - 1>();
-    float s1 = 0.0f, s2 = 0.0f;
+    const f32x2 minus = twice(-mean), r2 = twice(rstd);
+    f32x2 xh[HOLD ? V : 1][4], d[HOLD ? V : 1][4];
+    f32x2 t1 = 0, t2 = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (j * nt + tid < KV) {
-        float x[8], dy[8], gf[8];
-        widen8<T>(norm_ring[(st * 2 * V + j) * nt + tid], x);
-        widen8<T>(norm_ring[(st * 2 * V + V + j) * nt + tid], dy);
-        widen8<T>(g[j], gf);
+        f32x2 dy[4];
+        f32x2(&xj)[4] = xh[HOLD ? j : 0];
+        f32x2(&dj)[4] = d[HOLD ? j : 0];
+        terms(j, minus, r2, xj, dj, dy);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = (x[i] - mean) * rstd, d = dy[i] * gf[i];
-          s1 += d;
-          s2 = fmaf(d, xh, s2);
+        for (int i = 0; i < 4; ++i) {
+          t1 = add_f32x2(t1, dj[i]);
+          t2 = fma_f32x2(dj[i], xj[i], t2);
           if constexpr (COLS) {
-            dg[8 * j + i] = fmaf(dy[i], xh, dg[8 * j + i]);
-            db[8 * j + i] += dy[i];
+            dg[j][i] = fma_f32x2(dy[i], xj[i], dg[j][i]);
+            db[j][i] = add_f32x2(db[j][i], dy[i]);
           }
         }
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (warps > 1) {
-      if (lane == 0) red[slot][warp] = make_float2(s1, s2);
-      __syncthreads();
-      const float2 t = (lane & 15) < warps ? red[slot][lane & 15] : make_float2(0.0f, 0.0f);
-      s1 = t.x;
-      s2 = t.y;
+    float s1 = lo_f(t1) + hi_f(t1), s2 = lo_f(t2) + hi_f(t2);
+    // both sums in one butterfly: s1 in the lower half of the warp, s2 in the upper
+    const bool upper = lane >= 16;
+    float t = (upper ? s2 : s1) + __shfl_xor_sync(0xffffffffu, upper ? s1 : s2, 16);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-      }
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (warps > 1) {
+      if ((lane & 15) == 0) red[slot][upper][warp] = t;
+      __syncthreads();
+      t = (lane & 15) < warps ? red[slot][upper][lane & 15] : 0.0f;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
       slot ^= 1;   // as in cta_reduce: one barrier a row, two rows of partial sums
     }
-    const float m1 = s1 * rK, m2 = s2 * rK;
+    s1 = __shfl_sync(0xffffffffu, t, 0);
+    s2 = __shfl_sync(0xffffffffu, t, 16);
+    const f32x2 m1 = twice(-s1 * rK), m2 = twice(-s2 * rK);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = j * nt + tid;
       if (v < KV) {
-        float x[8], dy[8], gf[8], o[8];
-        widen8<T>(norm_ring[(st * 2 * V + j) * nt + tid], x);
-        widen8<T>(norm_ring[(st * 2 * V + V + j) * nt + tid], dy);
-        widen8<T>(g[j], gf);
+        f32x2 dy[4], o[4];
+        f32x2(&xj)[4] = xh[HOLD ? j : 0];
+        f32x2(&dj)[4] = d[HOLD ? j : 0];
+        if constexpr (!HOLD) terms(j, minus, r2, xj, dj, dy);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = (x[i] - mean) * rstd;
-          o[i] = rstd * (fmaf(dy[i], gf[i], -m1) - xh * m2);
-        }
-        *reinterpret_cast<uint4*>(a.dX + row * a.K + 8 * static_cast<int64_t>(v)) = narrow8<T>(o);
+        for (int i = 0; i < 4; ++i) o[i] = mul_f32x2(r2, fma_f32x2(xj[i], m2, add_f32x2(dj[i], m1)));
+        *reinterpret_cast<uint4*>(a.dX + row * a.K + 8 * static_cast<int64_t>(v)) = narrow8x2<T>(o);
       }
     }
     if (++st == NORM_STAGES) st = 0;
@@ -298,35 +352,42 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_bwd(const NormBwdArgs
       const int v = j * nt + tid;
       if (v < KV) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *reinterpret_cast<float4*>(p + 8 * v + i) = make_float4(dg[8 * j + i], dg[8 * j + i + 1], dg[8 * j + i + 2], dg[8 * j + i + 3]);
-          *reinterpret_cast<float4*>(p + a.K + 8 * v + i) = make_float4(db[8 * j + i], db[8 * j + i + 1], db[8 * j + i + 2], db[8 * j + i + 3]);
+        for (int i = 0; i < 4; i += 2) {
+          *reinterpret_cast<float4*>(p + 8 * v + 2 * i) = make_float4(lo_f(dg[j][i]), hi_f(dg[j][i]), lo_f(dg[j][i + 1]), hi_f(dg[j][i + 1]));
+          *reinterpret_cast<float4*>(p + a.K + 8 * v + 2 * i) = make_float4(lo_f(db[j][i]), hi_f(db[j][i]), lo_f(db[j][i + 1]), hi_f(db[j][i + 1]));
         }
       }
     }
   }
 }
 
-// dgamma and dbeta from the CTAs' column sums: 32 columns a CTA, its 16 warps
+// dgamma and dbeta from the CTAs' column sums: 128 columns a CTA, its 16 warps
 // take every 16th partial row each and are added in warp order, so the result
 // does not depend on timing. Launched as a programmatic dependent.
 template <typename T>
 __global__ void __launch_bounds__(512) k_norm_bwd_cols(const float* part, int64_t K, int ctas, uint16_t* dgamma, uint16_t* dbeta) {
-  __shared__ float red[16][32];
+  __shared__ float4 red[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // < 2 K: K % 16 == 0
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + 4 * lane;   // K % 16 == 0: a thread's columns are of one kind
   griddep_wait();
-  float s = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < ctas; i += 16) s += part[static_cast<int64_t>(i) * 2 * K + c];
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c < 2 * K) {
+#pragma unroll 8
+    for (int i = warp; i < ctas; i += 16) {
+      const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * 2 * K + c);
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
+  }
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0) {
-    s = red[0][lane];
+  if (warp == 0 && c < 2 * K) {
 #pragma unroll
-    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    for (int w = 1; w < 16; ++w) {
+      const float4 v = red[w][lane];
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
     uint16_t* out = c < K ? dgamma : dbeta;
-    if (out != nullptr) out[c < K ? c : c - K] = from_f<T>(s);
+    if (out != nullptr) *reinterpret_cast<uint2*>(out + (c < K ? c : c - K)) = make_uint2(narrow2<T>(s.x, s.y), narrow2<T>(s.z, s.w));
   }
 }
 

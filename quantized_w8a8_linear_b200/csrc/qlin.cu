@@ -1416,9 +1416,10 @@ qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   qlin_status s = device_info(&d);
   if (s != QLIN_OK) return s;
   const int64_t KV = a.K / 8;
-  // two vectors of a row per thread while there are rows for every SM to
-  // overlap, one when a row's latency counts (and 16 warps a row at most)
-  const int64_t want = a.M >= 4 * d->sms ? 2 : 1;
+  // four vectors of a row per thread while there are rows for every SM to
+  // overlap, one when a row's latency counts (and 16 warps a row at most):
+  // 16640 rows of 4096 took 41 us with four, 52 with two, 44 with eight
+  const int64_t want = a.M >= 4 * d->sms ? 4 : 1;
   const int64_t warps = std::min<int64_t>(std::max<int64_t>((KV + 32 * want - 1) / (32 * want), 1), NORM_MAX_THREADS / 32);
   const int64_t per = (KV + 32 * warps - 1) / (32 * warps);
   const int threads = static_cast<int>(32 * warps);
@@ -1428,12 +1429,12 @@ qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   return launch_norm_fwd_v<T, 8, OUT>(a, threads, d->sms, st);
 }
 
-template <typename T, int V, bool COLS>
+template <typename T, int V, bool COLS, int MAXT>
 qlin_status launch_norm_bwd_v(const NormBwdArgs& a, int threads, int sms, int64_t& ctas, cudaStream_t st) {
-  auto kern = k_norm_bwd<T, V, COLS>;
+  auto kern = k_norm_bwd<T, V, COLS, MAXT>;
   const int smem = NORM_STAGES * 2 * V * threads * 16;
   static std::atomic<bool> set[16] = {};
-  qlin_status s = allow_smem(kern, NORM_STAGES * 2 * V * NORM_MAX_THREADS * 16, set);
+  qlin_status s = allow_smem(kern, NORM_STAGES * 2 * V * MAXT * 16, set);
   if (s != QLIN_OK) return s;
   int per_sm = 0;
   s = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem), "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
@@ -1450,19 +1451,22 @@ qlin_status norm_bwd(const NormBwdArgs& a, void* dgamma, void* dbeta, cudaStream
   qlin_status s = device_info(&d);
   if (s != QLIN_OK) return s;
   const int64_t KV = a.K / 8;
-  const int64_t V = std::max<int64_t>((KV + NORM_MAX_THREADS - 1) / NORM_MAX_THREADS, 1);
+  // two vectors of a row a thread, more only for rows over 8192 wide: 16640
+  // rows of 4096 took 70 us with two (256 threads, two CTAs an SM), 90 with
+  // one, 83 with four
+  const int64_t V = std::max<int64_t>((KV + NORM_MAX_THREADS - 1) / NORM_MAX_THREADS, 2);
   const int threads = static_cast<int>((KV + 32 * V - 1) / (32 * V) * 32);
   int64_t ctas = 0;
-#define QLIN_NORM_BWD(v)                                                          \
-  s = a.part != nullptr ? launch_norm_bwd_v<T, v, true>(a, threads, d->sms, ctas, st) \
-                        : launch_norm_bwd_v<T, v, false>(a, threads, d->sms, ctas, st)
-  if (V == 1) QLIN_NORM_BWD(1);
-  else if (V == 2) QLIN_NORM_BWD(2);
-  else if (V == 3) QLIN_NORM_BWD(3);
-  else QLIN_NORM_BWD(4);
+#define QLIN_NORM_BWD(v, maxt)                                                          \
+  s = a.part != nullptr ? launch_norm_bwd_v<T, v, true, maxt>(a, threads, d->sms, ctas, st) \
+                        : launch_norm_bwd_v<T, v, false, maxt>(a, threads, d->sms, ctas, st)
+  if (V == 2 && threads <= 256) QLIN_NORM_BWD(2, 256);
+  else if (V == 2) QLIN_NORM_BWD(2, 512);
+  else if (V == 3) QLIN_NORM_BWD(3, 512);
+  else QLIN_NORM_BWD(4, 512);
 #undef QLIN_NORM_BWD
   if (s != QLIN_OK || a.part == nullptr) return s;
-  return launch_dependent(k_norm_bwd_cols<T>, "k_norm_bwd_cols launch", dim3(static_cast<unsigned>(2 * a.K / 32)), 512, 0, 1, st, static_cast<const float*>(a.part), a.K,
+  return launch_dependent(k_norm_bwd_cols<T>, "k_norm_bwd_cols launch", dim3(static_cast<unsigned>((2 * a.K + 127) / 128)), 512, 0, 1, st, static_cast<const float*>(a.part), a.K,
                           static_cast<int>(ctas), static_cast<uint16_t*>(dgamma), static_cast<uint16_t*>(dbeta));
 }
 
