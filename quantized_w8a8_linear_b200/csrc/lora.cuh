@@ -1005,17 +1005,20 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
             } else {
               const int sh = shift_of(row, n0);
               const int cols = N - col < 64 ? N - col : 64;
-              // elements [e0, e0 + 8) of the warp's 64 lie in one chunk; with a shift, the last lane has the first and last pieces
-              const int e0 = sh == 0 ? 8 * c : 8 * c + (16 - sh) / 2;
-              if (e0 + 8 <= 64 && e0 + 8 <= cols) {
-                *reinterpret_cast<uint4*>(dst + 2 * e0) = *reinterpret_cast<const uint4*>(src + sh + 2 * e0);
-              } else {
-                for (int e = e0; e < 64 && e < cols; ++e)
-                  *reinterpret_cast<uint16_t*>(dst + 2 * e) = *reinterpret_cast<const uint16_t*>(src + sh + 2 * e);
+              // with a shift, the piece has `head` elements before its first whole
+              // chunk and 8 - head behind its last one: one of the eight for each lane
+              const int head = (16 - sh) / 2 & 7, e0 = 8 * c + head;
+              auto element = [&](int e) {
+                if (e < cols) *reinterpret_cast<uint16_t*>(dst + 2 * e) = *reinterpret_cast<const uint16_t*>(src + sh + 2 * e);
+              };
+              if (head == 0 || c < 7) {
+                if (e0 + 8 <= cols) {
+                  *reinterpret_cast<uint4*>(dst + 2 * e0) = *reinterpret_cast<const uint4*>(src + sh + 2 * e0);
+                } else {
+                  for (int e = e0; e < e0 + 8; ++e) element(e);   // the matrix's last columns
+                }
               }
-              if (sh != 0 && c == 7)
-                for (int e = 0; e < (16 - sh) / 2 && e < cols; ++e)
-                  *reinterpret_cast<uint16_t*>(dst + 2 * e) = *reinterpret_cast<const uint16_t*>(src + sh + 2 * e);
+              if (head != 0) element(c < head ? c : 56 + c);
             }
           }
         }
@@ -1265,7 +1268,20 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       drain_mma(drain_bar);
     }
   } else if (warp < 9) {
-    // ---------------- epilogue, once per segment ----------------
+    // ---------------- zeros for adapters without rows; then the epilogue, once per segment ----------------
+    const int L = static_cast<int>(p.plan.L);
+    for (int a0 = 0; a0 < L; a0 += 32)
+    for (uint32_t empty = __ballot_sync(0xffffffffu, a0 + lane < L && (un.tiles == 0 || p.plan.tile0()[a0 + lane] == p.plan.tile0()[a0 + lane + 1]));
+         empty != 0; empty &= empty - 1) {
+      const int a = a0 + __ffs(empty) - 1;
+      for (int side = 0; side < 2; ++side) {
+        // an adapter's dA or dB is contiguous: 16-byte pieces, dealt out over the CTAs
+        const int64_t pieces = (side ? p.cols[1] : p.cols[0]) * p.R / 8;
+        uint4* out = reinterpret_cast<uint4*>(side ? p.out[1] : p.out[0]) + a * pieces;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x - 32 * 5; i < pieces; i += static_cast<int64_t>(gridDim.x) * 128)
+          out[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
     const int q = warp & 3;
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1381,8 +1397,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   }
 }
 
-// The segments k_lora_wgrad cut between CTAs, added in CTA order, and zeros
-// for adapters without rows. A CTA takes 8 values of R of 256 columns; blockIdx.x
+// The segments k_lora_wgrad cut between CTAs, added in CTA order. A CTA takes 8 values of R of 256 columns; blockIdx.x
 // names the boundary between two CTAs' ranges.
 __global__ void __launch_bounds__(LORA_WG_COLS) k_lora_wgrad_join(const LoraWgradParams p) {
   using T = __nv_bfloat16;
@@ -1417,11 +1432,6 @@ __global__ void __launch_bounds__(LORA_WG_COLS) k_lora_wgrad_join(const LoraWgra
       for (int i = 0; i < 8; ++i) f[i] *= s;
       write(a, cg, f);
     }
-  }
-  const float zero[8] = {};
-  for (int a = 0; a < p.plan.L; ++a) {
-    if (un.tiles > 0 && p.plan.tile0()[a] < p.plan.tile0()[a + 1]) continue;
-    for (int cg = static_cast<int>(blockIdx.x); cg < un.cgs; cg += static_cast<int>(gridDim.x)) write(a, cg, zero);
   }
 }
 

@@ -1626,11 +1626,12 @@ qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, c
   constexpr int smem = LoraShrinkSmem<RB>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  // the largest cluster whose CTAs are resident together (two per SM) when the
-  // tiles are full, and that leaves every CTA a block of the contraction
-  const int64_t full = (c.M + LORA_TILE - 1) / LORA_TILE;
+  // the largest cluster whose CTAs are resident together (two per SM), and that
+  // leaves every CTA a block of the contraction. The host does not know the
+  // number of tiles: full ones, and half a tile for each adapter but one.
+  const int64_t tiles = (c.M + LORA_TILE - 1) / LORA_TILE + (std::min(c.L, c.M) - 1) / 2;
   int cluster = 8;
-  while (cluster > 1 && (full * cluster > 2 * c.d->sms || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
+  while (cluster > 1 && (tiles * cluster > 2 * c.d->sms || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
   LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), static_cast<const uint16_t*>(X), scale, H, sp.Hs, sp.G, sp.Gs};
   return launch_dependent(kern, "k_lora_shrink launch", dim3(static_cast<unsigned>(lora_max_tiles(c.M, c.L) * cluster)), LORA_SHRINK_THREADS, smem, cluster, c.st, tw, p, cluster);
 }
@@ -1683,8 +1684,14 @@ qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const
   constexpr int smem = LoraWgradSmem<RB>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  LoraWgradParams p{c.view(), static_cast<int>(c.R), lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dHs, Hs}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
+  // Up to 1024 rows, a CTA for each 256 columns: no sum is cut, and there is
+  // nothing to join (512 x 4096 -> 4096, rank 16: 7 us less); beyond, one CTA
+  // per SM with equal ranges.
+  const int64_t cgs = (K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS;
+  const bool whole = c.M <= 1024 && cgs <= (1 << 20);
+  LoraWgradParams p{c.view(), static_cast<int>(c.R), whole ? static_cast<int>(cgs) : lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dHs, Hs}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
   QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", dim3(static_cast<unsigned>(p.ctas)), LORA_WG_THREADS, smem, 1, c.st, p));
+  if (whole) return QLIN_OK;
   return launch_dependent(k_lora_wgrad_join, "k_lora_wgrad_join launch", dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(c.R / 8)), LORA_WG_COLS, 0, 1,
                           c.st, p);
 }
