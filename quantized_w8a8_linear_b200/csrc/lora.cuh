@@ -470,9 +470,14 @@ struct LoraShrinkParams {
   uint16_t* Gs;         // [M,2,R]
 };
 
-template <int RB>   // ceil(R / 64)
+// RB: ceil(R / 64). DEEP: one CTA an SM with four stages, for tiles enough to
+// fill the SMs without clusters (16640 x 4096 rows at rank 64: 30 us against
+// 36 with two CTAs of two stages each); else two CTAs an SM, in clusters (64
+// tiles of 12288: 47 us in clusters of four, 52 with one deep CTA in clusters
+// of two). Above rank 64 a stage is larger: three of them, one CTA.
+template <int RB, bool DEEP>
 struct LoraShrinkSmem {
-  static constexpr int STAGES = RB == 1 ? 2 : 3;   // two CTAs an SM, or one
+  static constexpr int STAGES = RB == 2 ? 3 : DEEP ? 4 : 2;
   static constexpr int A_BYTES = 2 * LORA_TILE * 128;   // two halves of 64 columns
   static constexpr int W_BYTES = 2 * RB * 64 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
@@ -482,10 +487,10 @@ struct LoraShrinkSmem {
   static_assert(LORA_TILE * (RB * 64 + 4) * 4 <= STAGES * STAGE_BYTES, "partial tile");
 };
 
-template <typename T, int RB, bool W_MN>
+template <typename T, int RB, bool W_MN, bool DEEP>
 __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     k_lora_shrink(const __grid_constant__ CUtensorMap tmW, const LoraShrinkParams p, const int cluster) {
-  using S = LoraShrinkSmem<RB>;
+  using S = LoraShrinkSmem<RB, DEEP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto sA = [&](int s) { return smem + s * S::STAGE_BYTES; };

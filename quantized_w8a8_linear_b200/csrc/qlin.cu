@@ -1549,8 +1549,7 @@ qlin_status qlin_layer_norm_backward(const void* dY, const void* X, qlin_dtype x
     return ok();
   }
   QLIN_REQ_PTR(dY, "dY");
-  QLIN_REQ_PTR(mean, "mean");
-  QLIN_REQ_PTR(rstd, "rstd");
+  if (mean == nullptr || rstd == nullptr) return fail(QLIN_ERR_INVALID_ARG, "mean or rstd is NULL");
   QLIN_REQ_PTR(dX, "dX");
   if (cols) {
     if (workspace == nullptr || ws_bytes < qlin_workspace_bytes(QLIN_OP_LAYER_NORM_BACKWARD, M, 0, K))
@@ -1617,27 +1616,31 @@ struct LoraSplit {   // the backward pass's split rows
 };
 
 // H [M,R] = scale * X W^T; X [M,C]. W_MN: W is B [L,C,R], else A [L,R,C].
-template <typename T, int RB, bool W_MN>
-qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp) {
+template <typename T, int RB, bool W_MN, bool DEEP>
+qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp, int64_t tiles) {
   CUtensorMap tw;
   if (W_MN) QLIN_TRY(make_tmap_adapters(&tw, W, c.L, C, c.R, LORA_SHRINK_BK));
   else QLIN_TRY(make_tmap_adapters(&tw, W, c.L, c.R, C, static_cast<int>(round_up(c.R, 16))));
-  auto kern = k_lora_shrink<T, RB, W_MN>;
-  constexpr int smem = LoraShrinkSmem<RB>::TOTAL;
+  auto kern = k_lora_shrink<T, RB, W_MN, DEEP>;
+  constexpr int smem = LoraShrinkSmem<RB, DEEP>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  // the largest cluster whose CTAs are resident together (two per SM), and that
-  // leaves every CTA a block of the contraction. The host does not know the
-  // number of tiles: full ones, and half a tile for each adapter but one.
-  const int64_t tiles = (c.M + LORA_TILE - 1) / LORA_TILE + (std::min(c.L, c.M) - 1) / 2;
+  // the largest cluster whose CTAs are resident together, and that leaves every
+  // CTA a block of the contraction
+  const int64_t slots = (RB == 2 || DEEP ? 1 : 2) * c.d->sms;
   int cluster = 8;
-  while (cluster > 1 && (tiles * cluster > 2 * c.d->sms || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
+  while (cluster > 1 && (tiles * cluster > slots || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
   LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), static_cast<const uint16_t*>(X), scale, H, sp.Hs, sp.G, sp.Gs};
   return launch_dependent(kern, "k_lora_shrink launch", dim3(static_cast<unsigned>(lora_max_tiles(c.M, c.L) * cluster)), LORA_SHRINK_THREADS, smem, cluster, c.st, tw, p, cluster);
 }
 template <typename T, bool W_MN>
 qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp = {}) {
-  return c.R <= 64 ? launch_lora_shrink_rb<T, 1, W_MN>(c, X, C, W, scale, H, sp) : launch_lora_shrink_rb<T, 2, W_MN>(c, X, C, W, scale, H, sp);
+  // The host does not know the number of tiles: full ones, and half a tile for
+  // each adapter but one.
+  const int64_t tiles = (c.M + LORA_TILE - 1) / LORA_TILE + (std::min(c.L, c.M) - 1) / 2;
+  if (c.R > 64) return launch_lora_shrink_rb<T, 2, W_MN, false>(c, X, C, W, scale, H, sp, tiles);
+  if (2 * tiles > c.d->sms) return launch_lora_shrink_rb<T, 1, W_MN, true>(c, X, C, W, scale, H, sp, tiles);
+  return launch_lora_shrink_rb<T, 1, W_MN, false>(c, X, C, W, scale, H, sp, tiles);
 }
 
 // Y [M,N] += scale * H V^T. V_MN: V is A [L,R,N], else B [L,N,R].
