@@ -221,12 +221,16 @@ struct NormBwdArgs {
   const float* rstd;       // [M]
   uint16_t* dX;            // [M,K]
   float* part;             // [CTAs][2][K] column sums of each CTA, or nullptr
+  int row_threads;         // threads of a row: all of the CTA's, or 32 (each warp a row of its own)
 };
 
 // The two row sums need no second pass: with mean and rstd given, sum d and
 // sum d * xh are reduced behind one barrier. Each thread keeps the column
 // sums of its own 8 V columns in registers over all rows of its CTA and
-// writes them once at the end, for k_norm_bwd_cols to add in CTA order.
+// writes them once at the end, for k_norm_bwd_cols to add in CTA order. Rows
+// of up to 1024 take a warp each, whose column sums the CTA adds first: the
+// second kernel then reads a row of sums for each CTA, not for each warp
+// (16640 rows of 160: 26 us with a CTA of one warp a row).
 // MAXT: the threads of a row at most (256 or 512); 512 of them an SM, so that
 // the compiler may spread a row's independent work over 128 registers (left to
 // itself, at 110, 16640 rows of 4096 took 87 us instead of 70).
@@ -234,22 +238,23 @@ template <typename T, int V, bool COLS, int MAXT>
 __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs a) {
   extern __shared__ uint4 norm_ring[];   // [NORM_STAGES][2 V][threads]: x, dy
   __shared__ float red[2][2][16];
-  const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = nt >> 5;
+  const int nt = a.row_threads, group = threadIdx.x / nt, tid = threadIdx.x % nt, warp = tid >> 5, lane = tid & 31, warps = nt >> 5;
+  const int groups = blockDim.x / nt, bt = blockDim.x;   // groups > 1: one warp each, no barrier in the loop
   const int KV = static_cast<int>(a.K / 8);
-  const int64_t step = gridDim.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups, row0 = static_cast<int64_t>(blockIdx.x) * groups + group;
   auto fetch = [&](int64_t row, int st) {
     if (row < a.M) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int v = j * nt + tid;
         const int64_t at = row * a.K + 8 * static_cast<int64_t>(v);
-        cp_async16(&norm_ring[(st * 2 * V + j) * nt + tid], a.X + at, v < KV);
-        cp_async16(&norm_ring[(st * 2 * V + V + j) * nt + tid], a.dY + at, v < KV);
+        cp_async16(&norm_ring[(st * 2 * V + j) * bt + threadIdx.x], a.X + at, v < KV);
+        cp_async16(&norm_ring[(st * 2 * V + V + j) * bt + threadIdx.x], a.dY + at, v < KV);
       }
     }
     cp_async_commit();
   };
-  for (int i = 0; i < NORM_STAGES - 1; ++i) fetch(blockIdx.x + i * step, i);
+  for (int i = 0; i < NORM_STAGES - 1; ++i) fetch(row0 + i * step, i);
   // up to two vectors a thread: gamma widened, and a row's xh and d kept from
   // the sums to the output; beyond that both are formed again from the ring
   constexpr bool HOLD = V <= 2;
@@ -268,8 +273,8 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs
   int st = 0, slot = 0;
   // xh and d of vector j; dy on the way
   auto terms = [&](int j, const f32x2& minus, const f32x2& r2, f32x2 (&xh)[4], f32x2 (&d)[4], f32x2 (&dy)[4]) {
-    widen8x2<T>(norm_ring[(st * 2 * V + j) * nt + tid], xh);
-    widen8x2<T>(norm_ring[(st * 2 * V + V + j) * nt + tid], dy);
+    widen8x2<T>(norm_ring[(st * 2 * V + j) * bt + threadIdx.x], xh);
+    widen8x2<T>(norm_ring[(st * 2 * V + V + j) * bt + threadIdx.x], dy);
     f32x2 gj[4];
     if constexpr (!HOLD) widen8x2<T>(g[HOLD ? 0 : j], gj);
 #pragma unroll
@@ -279,11 +284,11 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs
     }
   };
   float next_mean = 0.0f, next_rstd = 0.0f;   // looked up a row ahead
-  if (blockIdx.x < a.M) {
-    next_mean = __ldg(a.mean + blockIdx.x);
-    next_rstd = __ldg(a.rstd + blockIdx.x);
+  if (row0 < a.M) {
+    next_mean = __ldg(a.mean + row0);
+    next_rstd = __ldg(a.rstd + row0);
   }
-  for (int64_t row = blockIdx.x; row < a.M; row += step) {
+  for (int64_t row = row0; row < a.M; row += step) {
     const float mean = next_mean, rstd = next_rstd;
     if (row + step < a.M) {
       next_mean = __ldg(a.mean + row + step);
@@ -347,15 +352,28 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs
   cp_async_wait<0>();
   if constexpr (COLS) {
     float* p = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.K;
+    float* mine = p;
+    if (groups > 1) {   // the ring's memory, when every warp is done with it: [groups][2][K], which 3072 V bytes a warp hold up to K = 384 V
+      __syncthreads();
+      mine = reinterpret_cast<float*>(norm_ring) + static_cast<int64_t>(group) * 2 * a.K;
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = j * nt + tid;
       if (v < KV) {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          *reinterpret_cast<float4*>(p + 8 * v + 2 * i) = make_float4(lo_f(dg[j][i]), hi_f(dg[j][i]), lo_f(dg[j][i + 1]), hi_f(dg[j][i + 1]));
-          *reinterpret_cast<float4*>(p + a.K + 8 * v + 2 * i) = make_float4(lo_f(db[j][i]), hi_f(db[j][i]), lo_f(db[j][i + 1]), hi_f(db[j][i + 1]));
+          *reinterpret_cast<float4*>(mine + 8 * v + 2 * i) = make_float4(lo_f(dg[j][i]), hi_f(dg[j][i]), lo_f(dg[j][i + 1]), hi_f(dg[j][i + 1]));
+          *reinterpret_cast<float4*>(mine + a.K + 8 * v + 2 * i) = make_float4(lo_f(db[j][i]), hi_f(db[j][i]), lo_f(db[j][i + 1]), hi_f(db[j][i + 1]));
         }
+      }
+    }
+    if (groups > 1) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < 2 * a.K; c += bt) {
+        float t = 0.0f;
+        for (int g0 = 0; g0 < groups; ++g0) t += reinterpret_cast<const float*>(norm_ring)[static_cast<int64_t>(g0) * 2 * a.K + c];
+        p[c] = t;
       }
     }
   }

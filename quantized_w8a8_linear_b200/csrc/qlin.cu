@@ -550,8 +550,8 @@ qlin_status int8_outlier_gemm_ws(qlin_dtype xdt, int64_t M, int64_t K, const int
 }
 
 // CTAs of k_norm_bwd at most: each leaves 2 K fp32 column sums for the second
-// kernel, so wide rows take two CTAs per SM and short ones as many as fit.
-int64_t norm_bwd_ctas(int64_t K) { return std::min<int64_t>(std::max<int64_t>((int64_t{1} << 20) / K, 296), 4736); }
+// kernel, so wide rows take two CTAs per SM, narrower ones four.
+int64_t norm_bwd_ctas(int64_t K) { return K > 1024 && K < 3500 ? 592 : 296; }
 
 #define QLIN_TRY(...)                  \
   do {                                 \
@@ -1430,7 +1430,7 @@ qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
 }
 
 template <typename T, int V, bool COLS, int MAXT>
-qlin_status launch_norm_bwd_v(const NormBwdArgs& a, int threads, int sms, int64_t& ctas, cudaStream_t st) {
+qlin_status launch_norm_bwd_v(NormBwdArgs a, int threads, int groups, int sms, int64_t& ctas, cudaStream_t st) {
   auto kern = k_norm_bwd<T, V, COLS, MAXT>;
   const int smem = NORM_STAGES * 2 * V * threads * 16;
   static std::atomic<bool> set[16] = {};
@@ -1440,7 +1440,8 @@ qlin_status launch_norm_bwd_v(const NormBwdArgs& a, int threads, int sms, int64_
   s = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem), "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
   if (s != QLIN_OK) return s;
   if (per_sm < 1) return fail(QLIN_ERR_UNSUPPORTED, "layer norm's backward pass does not fit on an SM");
-  ctas = std::min<int64_t>(std::min<int64_t>(a.M, static_cast<int64_t>(per_sm) * sms), norm_bwd_ctas(a.K));
+  ctas = std::min<int64_t>(std::min<int64_t>((a.M + groups - 1) / groups, static_cast<int64_t>(per_sm) * sms), norm_bwd_ctas(a.K));
+  a.row_threads = threads / groups;
   kern<<<static_cast<unsigned>(ctas), threads, smem, st>>>(a);
   return check_cuda(cudaGetLastError(), "k_norm_bwd launch");
 }
@@ -1451,18 +1452,20 @@ qlin_status norm_bwd(const NormBwdArgs& a, void* dgamma, void* dbeta, cudaStream
   qlin_status s = device_info(&d);
   if (s != QLIN_OK) return s;
   const int64_t KV = a.K / 8;
-  // two vectors of a row a thread, more only for rows over 8192 wide: 16640
-  // rows of 4096 took 70 us with two (256 threads, two CTAs an SM), 90 with
-  // one, 83 with four
-  const int64_t V = std::max<int64_t>((KV + NORM_MAX_THREADS - 1) / NORM_MAX_THREADS, 2);
-  const int threads = static_cast<int>((KV + 32 * V - 1) / (32 * V) * 32);
+  // Rows of up to 1024: a warp each, eight a CTA. Wider ones: two vectors of a
+  // row a thread, more only over 8192 (16640 rows of 4096 took 70 us with two,
+  // 256 threads, two CTAs an SM; 90 with one, 83 with four).
+  const int groups = KV <= 128 && a.M > 1 ? 8 : 1;
+  const int64_t V = groups > 1 ? (KV <= 64 ? 2 : 4) : std::max<int64_t>((KV + NORM_MAX_THREADS - 1) / NORM_MAX_THREADS, 2);
+  const int threads = groups > 1 ? 32 * groups : static_cast<int>((KV + 32 * V - 1) / (32 * V) * 32);
   int64_t ctas = 0;
 #define QLIN_NORM_BWD(v, maxt)                                                          \
-  s = a.part != nullptr ? launch_norm_bwd_v<T, v, true, maxt>(a, threads, d->sms, ctas, st) \
-                        : launch_norm_bwd_v<T, v, false, maxt>(a, threads, d->sms, ctas, st)
+  s = a.part != nullptr ? launch_norm_bwd_v<T, v, true, maxt>(a, threads, groups, d->sms, ctas, st) \
+                        : launch_norm_bwd_v<T, v, false, maxt>(a, threads, groups, d->sms, ctas, st)
   if (V == 2 && threads <= 256) QLIN_NORM_BWD(2, 256);
   else if (V == 2) QLIN_NORM_BWD(2, 512);
   else if (V == 3) QLIN_NORM_BWD(3, 512);
+  else if (threads <= 256) QLIN_NORM_BWD(4, 256);
   else QLIN_NORM_BWD(4, 512);
 #undef QLIN_NORM_BWD
   if (s != QLIN_OK || a.part == nullptr) return s;
@@ -1607,6 +1610,9 @@ struct LoraCall {
   DeviceInfo* d;
   cudaStream_t st;
   LoraPlan view() const { return LoraPlan{plan, M, L}; }
+  // The host does not know the number of tiles: full ones, and half a tile for
+  // each adapter but one.
+  int64_t tiles() const { return (M + LORA_TILE - 1) / LORA_TILE + (std::min(L, M) - 1) / 2; }
 };
 
 struct LoraSplit {   // the backward pass's split rows
@@ -1635,9 +1641,7 @@ qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, c
 }
 template <typename T, bool W_MN>
 qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp = {}) {
-  // The host does not know the number of tiles: full ones, and half a tile for
-  // each adapter but one.
-  const int64_t tiles = (c.M + LORA_TILE - 1) / LORA_TILE + (std::min(c.L, c.M) - 1) / 2;
+  const int64_t tiles = c.tiles();
   if (c.R > 64) return launch_lora_shrink_rb<T, 2, W_MN, false>(c, X, C, W, scale, H, sp, tiles);
   if (2 * tiles > c.d->sms) return launch_lora_shrink_rb<T, 1, W_MN, true>(c, X, C, W, scale, H, sp, tiles);
   return launch_lora_shrink_rb<T, 1, W_MN, false>(c, X, C, W, scale, H, sp, tiles);
@@ -1687,11 +1691,11 @@ qlin_status launch_lora_wgrad(const LoraCall& c, const void* X, int64_t K, const
   constexpr int smem = LoraWgradSmem<RB>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  // Up to 1024 rows, a CTA for each 256 columns: no sum is cut, and there is
+  // Up to eight tiles, a CTA for each 256 columns: no sum is cut, and there is
   // nothing to join (512 x 4096 -> 4096, rank 16: 7 us less); beyond, one CTA
   // per SM with equal ranges.
   const int64_t cgs = (K + LORA_WG_COLS - 1) / LORA_WG_COLS + (N + LORA_WG_COLS - 1) / LORA_WG_COLS;
-  const bool whole = c.M <= 1024 && cgs <= (1 << 20);
+  const bool whole = c.tiles() <= 8 && cgs <= (1 << 20);
   LoraWgradParams p{c.view(), static_cast<int>(c.R), whole ? static_cast<int>(cgs) : lora_wg_ctas(c.d), {K, N}, {static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(dY)}, {dHs, Hs}, c.scale, {static_cast<uint16_t*>(dA), static_cast<uint16_t*>(dB)}, part};
   QLIN_TRY(launch_dependent(kern, "k_lora_wgrad launch", dim3(static_cast<unsigned>(p.ctas)), LORA_WG_THREADS, smem, 1, c.st, p));
   if (whole) return QLIN_OK;
