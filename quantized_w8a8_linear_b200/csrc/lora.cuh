@@ -955,9 +955,15 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
         const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
         uint8_t* yr = sY(stage) + q * 32 * S::Y_ROW;   // the warp's rows
         const int shift = shift_of(my_row, n0);
-        uint8_t* mine = yr + lane * S::Y_ROW + 128 * half + (VEC ? 0 : shift & ~3);
-        const uint32_t odd = VEC ? 0 : (shift & 2) * 8;   // 16: pairs of columns straddle 32-bit words
-        uint32_t before = 0;                              // VEC false: the previous pair
+        // VEC false: the piece from the 8-byte word it starts in; `late`: it starts
+        // in that word's second half; `odd`: in the upper 16 bits of a 32-bit word,
+        // so that pairs of columns straddle two
+        uint8_t* mine = yr + lane * S::Y_ROW + 128 * half + (VEC ? 0 : shift & ~7);
+        const bool late = !VEC && (shift & 4) != 0;
+        const uint32_t odd = VEC ? 0 : (shift & 2) * 8;
+        uint2 carry = make_uint2(0, 0);              // the two words behind the ones done
+        uint32_t before = 0, last = 0;               // the previous pair, the word of it not yet written (late)
+        if constexpr (!VEC) carry = *reinterpret_cast<const uint2*>(mine);
 #pragma unroll
         for (int c = 0; c < 64; c += 16) {
           uint32_t v[16];
@@ -975,22 +981,45 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
               *at = narrow8<T>(f);
             }
           } else {
-            uint32_t* w = reinterpret_cast<uint32_t*>(mine + 2 * c);
+            // 8-byte accesses: rows 272 bytes apart meet in every eighth lane's
+            // banks, so 32-bit ones took four passes each (63% of the LSU's time)
+            uint2* at = reinterpret_cast<uint2*>(mine + 2 * c);   // words 0 .. 7, and the next two
+            uint32_t w[10] = {carry.x, carry.y};
+#pragma unroll
+            for (int i = 1; i < 5; ++i) {
+              carry = at[i];
+              w[2 * i] = carry.x;
+              w[2 * i + 1] = carry.y;
+            }
+            uint32_t sums[8];   // the words of the updated pairs, from word `late` on
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              // words not yet written: w[i + 1], and the upper half of w[i] (its lower half is the previous pair's)
-              const uint32_t pair = __funnelshift_r(w[i], odd ? w[i + 1] : 0u, odd);
+              const uint32_t lo = late ? w[i + 1] : w[i], hi = late ? w[i + 2 < 10 ? i + 2 : 9] : w[i + 1];
+              const uint32_t pair = __funnelshift_r(lo, hi, odd);
               const uint32_t sum = narrow2<T>(fmaf(sum_of(2 * i), s, to_f<T>(static_cast<uint16_t>(pair))),
-                                            fmaf(sum_of(2 * i + 1), s, to_f<T>(static_cast<uint16_t>(pair >> 16))));
-              if (odd && c + i == 0) reinterpret_cast<uint16_t*>(w)[1] = static_cast<uint16_t>(sum);   // the lower half is another warp's
-              else w[i] = __funnelshift_l(before, sum, odd);
+                                              fmaf(sum_of(2 * i + 1), s, to_f<T>(static_cast<uint16_t>(pair >> 16))));
+              sums[i] = __funnelshift_l(before, sum, odd);
               before = sum;
-              if (odd) {
-                // keep the second half of the pair where the next one, or another warp, leaves it alone
-                if (c + 2 * i == 62) reinterpret_cast<uint16_t*>(w)[2 * (i + 1)] = static_cast<uint16_t>(sum >> 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint2 two = late ? make_uint2(i == 0 ? last : sums[2 * i - 1], sums[2 * i]) : make_uint2(sums[2 * i], sums[2 * i + 1]);
+              if (c > 0 || i > 0) {
+                at[i] = two;
+              } else {   // the piece's first word: what lies before it is another warp's
+                uint32_t* first = reinterpret_cast<uint32_t*>(at) + late;
+                if (odd) reinterpret_cast<uint16_t*>(first)[1] = static_cast<uint16_t>(sums[0] >> 16);
+                else *first = sums[0];
+                if (!late) first[1] = sums[1];
               }
             }
+            last = sums[7];
           }
+        }
+        if constexpr (!VEC) {   // behind the last whole words; what lies after the piece is another warp's
+          uint32_t* end = reinterpret_cast<uint32_t*>(mine + 128);
+          if (late) *end++ = last;
+          if (odd) *reinterpret_cast<uint16_t*>(end) = static_cast<uint16_t>(before >> 16);
         }
         tc_fence_before();
         __syncwarp();
