@@ -26,7 +26,8 @@ from oracle import norm_lora as o
 pytestmark = pytest.mark.gpu
 
 U, D = 2.0 ** -24, 80
-SHAPES = [(1, 16), (1, 4096), (3, 48), (13, 1040), (37, 4096), (5, 8192), (600, 528), (700, 2064), (2, 32768), (9, 12288)]
+SHAPES = [(1, 16), (1, 4096), (3, 48), (13, 1040), (37, 4096), (5, 8192), (600, 528), (700, 2064), (2, 32768), (9, 12288),
+          (640, 4096), (650, 12304), (620, 32768), (1500, 16)]
 
 
 @pytest.fixture(scope="module")
@@ -146,7 +147,8 @@ def test_rows_with_nan_and_inf_stay_alone(q):
     assert torch.isnan(got[5]).all() and torch.isnan(got[20, 0])
 
 
-BWD = [(1, 16), (1, 4096), (13, 1040), (37, 4096), (5, 8192), (700, 528), (1500, 2064), (9, 12288), (3, 16384)]
+BWD = [(1, 16), (1, 4096), (13, 1040), (37, 4096), (5, 8192), (700, 528), (1500, 2064), (9, 12288), (3, 16384),
+       (2, 512), (9, 1024), (3000, 1008), (5000, 160), (2500, 496), (700, 4096), (350, 16384)]
 
 
 @pytest.mark.parametrize("M,K", BWD)

@@ -82,7 +82,12 @@ def _check_forward(c, Y, H, dtype):
 FWD = [(1, 16, 8, 1, 8, 0), (1, 64, 64, 1, 16, 0), (1, 4096, 1000, 2, 16, 1), (5, 80, 1, 3, 8, "tokens"), (7, 256, 65, 1, 128, "tokens"),
        (64, 1024, 264, 32, 16, "tokens"), (127, 208, 72, 2, 24, "spans"), (128, 512, 256, 1, 64, "spans"), (129, 512, 136, 2, 72, "tokens"),
        (130, 64, 515, 1, 40, "spans"), (300, 528, 63, 4, 120, "tokens"), (257, 1040, 200, 100, 8, "tokens"), (40, 128, 129, 1024, 8, "tokens"),
-       (33, 128, 64, 3, 16, -1), (1100, 144, 96, 2, 32, "spans")]
+       (33, 128, 64, 3, 16, -1), (1100, 144, 96, 2, 32, "spans"),
+       # both sides of the choice between the kernel of few rows and the tiles' (M <= 256, R <= 32, M R <= 4096)
+       (256, 128, 72, 3, 16, "tokens"), (257, 128, 72, 3, 16, "tokens"), (128, 96, 41, 2, 32, "tokens"), (129, 96, 41, 2, 32, "tokens"),
+       (60, 96, 41, 2, 40, "tokens"), (1, 32768, 16, 1, 32, 0), (9, 16, 3, 2, 8, "tokens"),
+       # tiles enough for one CTA an SM and no clusters
+       (9700, 144, 64, 3, 16, "spans")]
 
 
 @pytest.mark.parametrize("M,K,N,L,R,idx", FWD)
@@ -97,7 +102,9 @@ def test_forward(q, M, K, N, L, R, idx, dtype):
 BWD = [(1, 16, 8, 1, 8, 0), (1, 64, 64, 2, 16, 1), (5, 80, 8, 3, 8, "tokens"), (7, 256, 72, 1, 128, "tokens"), (64, 1024, 264, 32, 16, "tokens"),
        (127, 208, 72, 2, 24, "spans"), (128, 512, 256, 1, 64, "spans"), (129, 512, 136, 2, 72, "tokens"), (300, 528, 72, 4, 120, "tokens"),
        (257, 1040, 200, 100, 8, "tokens"), (40, 128, 136, 1024, 8, "tokens"), (33, 128, 64, 3, 16, -1), (1100, 144, 96, 2, 32, "spans"),
-       (1500, 272, 528, 1, 16, "spans"), (1300, 528, 272, 3, 128, "spans")]
+       (1500, 272, 528, 1, 16, "spans"), (1300, 528, 272, 3, 128, "spans"),
+       # gradients cut between CTAs: fewer units than CTAs, and more
+       (3000, 416, 680, 3, 32, "tokens"), (1200, 2064, 1304, 1, 72, "spans"), (2300, 1040, 2600, 5, 8, "tokens"), (9700, 80, 72, 2, 16, "spans")]
 
 
 @pytest.mark.parametrize("M,K,N,L,R,idx", BWD)
@@ -133,6 +140,16 @@ def test_backward(q, M, K, N, L, R, idx):
         assert (np.abs(g - w) <= e + half * (np.abs(w) + e)).all()
         empty = [l for l in range(L) if not (ix == l).any()]
         assert not g[empty].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_every_alignment_of_a_row(q, dtype):
+    # rows whose start is any even number of bytes past 16, whole and partial last columns
+    for N in list(range(120, 137)) + [1, 7, 63, 191, 193, 261]:
+        c = _case(300, 64, N, 3, 16, dtype, "tokens", 20)
+        H = torch.full((300, 16), 77.0, device="cuda")
+        Y, _, _ = _forward(q, c, H)
+        _check_forward(c, Y, H, dtype)
 
 
 def test_order_of_rows_does_not_matter(q):
