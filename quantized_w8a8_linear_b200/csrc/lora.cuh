@@ -335,10 +335,15 @@ __global__ void __launch_bounds__(LORA_ROWS_THREADS, 2) k_lora_rows(const LoraRo
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank()), R = p.R;
   griddep_wait();
+  // the octet's record is asked for beside the plan's header, not after it: the
+  // grid ends where the plan's room for octets does
   const int o = blockIdx.x / LORA_ROWS_CLUSTER;
+  const int4* record = reinterpret_cast<const int4*>(p.plan.octet(o));
+  const int4 head = record[0], rows0 = record[1], rows1 = record[2];
   if (o >= p.plan.tiles(true)) return;   // all CTAs of the cluster
+  const int a = head.x, n = head.y;
+  const int rows[8] = {rows0.x, rows0.y, rows0.z, rows0.w, rows1.x, rows1.y, rows1.z, rows1.w};
   const int* oct = p.plan.octet(o);
-  const int a = oct[0], n = oct[1];
   const int KV = static_cast<int>(p.K / 8), kvs = (KV + LORA_ROWS_CLUSTER - 1) / LORA_ROWS_CLUSTER;
   const int k0 = KV * rank / LORA_ROWS_CLUSTER, kn = KV * (rank + 1) / LORA_ROWS_CLUSTER - k0;
   const int n0 = static_cast<int>(p.N * rank / LORA_ROWS_CLUSTER), n1 = static_cast<int>(p.N * (rank + 1) / LORA_ROWS_CLUSTER);
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(LORA_ROWS_THREADS, 2) k_lora_rows(const LoraRo
   const float s = __ldg(p.scale + a);
   uint16_t* yr[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) yr[j] = p.Y + (j < n ? oct[4 + j] * p.N : 0);
+  for (int j = 0; j < 8; ++j) yr[j] = p.Y + (j < n ? rows[j] * p.N : 0);
   for (int col = n0 + tid; col < n1; col += 2 * LORA_ROWS_THREADS) {   // columns col and col + 256
     const bool two = col + LORA_ROWS_THREADS < n1;
     const int next = two ? col + LORA_ROWS_THREADS : col;
@@ -529,9 +534,15 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
 
   const int tile = blockIdx.x / cluster;
   const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+  // the tile's record and rows are asked for beside the plan's header, not
+  // after it: the grid ends where the plan's room for tiles does
+  const int* rows = p.plan.rows(tile);
+  const int2 info = p.plan.info(tile);
+  int src[16];   // a copying thread's rows: r0, r0 + 8, ...; M past the count
+#pragma unroll
+  for (int i = 0; i < 16; ++i) src[i] = warp < 4 ? rows[(threadIdx.x >> 4) + 8 * i] : 0;
   const bool work = tile < p.plan.tiles();   // the same in all CTAs of the cluster
-  const int2 info = work ? p.plan.info(tile) : make_int2(0, 0);
-  const int a = info.x, n = info.y;
+  const int a = info.x, n = work ? info.y : 0;
   const int kbs = static_cast<int>((p.C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK);
   const int kb0 = static_cast<int>(static_cast<int64_t>(kbs) * rank / cluster);
   const int kb1 = static_cast<int>(static_cast<int64_t>(kbs) * (rank + 1) / cluster);
@@ -540,11 +551,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
   if (work && warp < 4) {
     // ---------------- copies: chunk c of rows r0, r0 + 8, ..., 16 lanes a row ----------------
     const int c = lane & 15, r0 = threadIdx.x >> 4;
-    const int* rows = p.plan.rows(tile);
-    int src[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) src[i] = r0 + 8 * i < n ? rows[r0 + 8 * i] : -1;
-    const int C = static_cast<int>(p.C);
+    const int C = static_cast<int>(p.C), M = static_cast<int>(p.plan.M);
     const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128 + (((c & 7) ^ r0) << 4));
     int stage = 0;
     uint32_t phase = 0, issued = 0;
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
       const uint8_t* x = reinterpret_cast<const uint8_t*>(p.X + kb * LORA_SHRINK_BK + 8 * c);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (src[i] >= 0) cp_async16_or_zero(d + 1024u * i, x + row_bytes(src[i], 2 * C), in);
+        if (src[i] < M) cp_async16_or_zero(d + 1024u * i, x + row_bytes(src[i], 2 * C), in);
       cp_async_arrive(&full_bar[stage]);
       issued |= 1u << stage;
       if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
@@ -775,17 +782,16 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     // ---------------- copies of Y: chunk c of rows r0, r0 + 8, ..., 16 lanes a row ----------------
     const int c = lane & 15, r0 = threadIdx.x >> 4;
     const int64_t all = 2 * p.plan.M * p.N;   // bytes of Y
-    const int row_size = static_cast<int>(2 * p.N);
+    const int row_size = static_cast<int>(2 * p.N), M = static_cast<int>(p.plan.M);
     const uint8_t* Y = reinterpret_cast<const uint8_t*>(p.Y);
     int rows[16];
-    int stage = 0, n = 0;
+    int stage = 0;
     uint32_t phase = 0;
     bool good = true, next = true;
     for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
       if (next) {
-        n = p.plan.info(static_cast<int>(t)).y;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) rows[i] = r0 + 8 * i < n ? p.plan.rows(static_cast<int>(t))[r0 + 8 * i] : -1;
+        for (int i = 0; i < 16; ++i) rows[i] = p.plan.rows(static_cast<int>(t))[r0 + 8 * i];   // M past the count
       }
       good = __all_sync(0xffffffffu, mbar_wait(&yempty_bar[stage], phase ^ 1u, abort_flag));
       if (!good) break;
@@ -794,7 +800,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
       const uint32_t d = smem_u32(sY(stage)) + r0 * S::Y_ROW;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (rows[i] >= 0) {
+        if (rows[i] < M) {
           const int64_t b = row_bytes(rows[i], row_size) + 2 * n0;
           const int shift = VEC ? 0 : static_cast<int>(b & 15);
           const int64_t at = b - shift + 16 * c;
@@ -888,8 +894,9 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
       if (next) {
         const int2 info = p.plan.info(static_cast<int>(t));
+        const int at = p.plan.rows(static_cast<int>(t))[q * 32 + lane];
         n = info.y - q * 32;
-        my_row = n > lane ? p.plan.rows(static_cast<int>(t))[q * 32 + lane] : 0;
+        my_row = n > lane ? at : 0;
         if (u == u0) {
           griddep_wait();    // H
         } else {             // the MMAs that read the previous tile's parts
