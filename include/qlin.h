@@ -278,8 +278,8 @@ QLIN_API qlin_status qlin_int8_block_forward(const void *X, qlin_dtype xdt, int6
  * gamma, beta [K] in xdt, each nullable (1 and 0: the form whose scale and
  * shift come from a modulation, or are folded into it). mean, rstd fp32 [M],
  * each nullable: kept for the backward pass. eps >= 0. Y may be X.
- * Same shape and alignment rules as the linears (gamma, beta 16-byte aligned;
- * mean and rstd have no alignment rule here). */
+ * Same shape and alignment rules as the linears; mean and rstd, here and in
+ * the backward pass, only need the alignment of a float. */
 QLIN_API qlin_status qlin_layer_norm_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *gamma,
                                     const void *beta, float eps, void *Y, float *mean, float *rstd,
                                     void *stream);
@@ -337,7 +337,7 @@ QLIN_API qlin_status qlin_lora_plan(const int32_t *idx, int64_t M, int64_t L, vo
  * parts (16 significant bits in bf16, 22 in fp16); all sums are fp32 and Y is
  * rounded once. R % 8 == 0, 8 <= R <= 128; N is arbitrary up to 2^28. A row's result does
  * not depend on the other rows of the batch beyond the order in which its K
- * products are added. */
+ * products are added. Y and H overlap no other argument. */
 QLIN_API qlin_status qlin_lora_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A, const void *B,
                               const float *scale, int64_t L, int64_t R, int64_t N, const void *plan,
                               size_t plan_bytes, float *H, void *Y, void *stream);
@@ -353,7 +353,8 @@ QLIN_API size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R);
  *           over the adapter's rows; zeros for an adapter without rows.
  * dA and dB are written, not added to, in an order of sums that does not
  * depend on timing. xdt must be QLIN_BF16 (the parts of dH need fp32's
- * exponent range); N % 8 == 0. M = 0 writes zeros to dA and dB. */
+ * exponent range); N % 8 == 0. M = 0 writes zeros to dA and dB. Outputs
+ * overlap no other argument. */
 QLIN_API qlin_status qlin_lora_backward(const void *dY, const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A,
                                const void *B, const float *scale, int64_t L, int64_t R, int64_t N,
                                const void *plan, size_t plan_bytes, const float *H, void *dX, void *dA,

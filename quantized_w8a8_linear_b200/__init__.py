@@ -12,6 +12,15 @@ Functions keep the C names:
     Wq8, s8 = qlin_quantize_weight(W, QLIN_W_FP8_TENSOR)
     xs = qlin_calibrate_input_scale(X_calibration)
     Y = qlin_fp8_forward(X, Wq8, s8, QLIN_W_FP8_TENSOR, x_scale=xs)
+
+Beside the projections, layer norm (straight to their codes, if wanted) and
+low-rank adapters of many requests, with their gradients:
+
+    Xq, s_x = qlin_layer_norm_fp8_prep(X, gamma, beta)
+    Y = qlin_fp8_gemm(Xq, s_x, Wq8, s8, QLIN_W_FP8_CHANNEL, X.dtype)
+    plan = qlin_lora_plan(adapter_of_row, L)            # once per batch
+    qlin_lora_forward(Xn, A, B, scale, plan, Y, H=H)    # Y += s (Xn A^T) B^T, in place
+    dX, dA, dB = qlin_lora_backward(dY, Xn, A, B, scale, plan, H, dX=dX)
 """
 from __future__ import annotations
 

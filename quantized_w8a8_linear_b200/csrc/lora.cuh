@@ -304,7 +304,9 @@ __device__ __forceinline__ void store_split4(uint16_t* row, int R, const float4&
 // column. Latency is all that counts here (64 rows of 32 adapters of rank 16
 // move 20 MB, 3 us of HBM time): the CTAs ask for their part of B and Y into
 // L2 before they turn to A, and there is no second launch. fp32 FMAs: at these
-// sizes the tensor cores would wait for the same bytes.
+// sizes the tensor cores would wait for the same bytes. One row 4096 -> 4096
+// at rank 16 takes 6 us in a graph of such calls (10 through the two kernels
+// below), 64 rows of 32 adapters 7 (19).
 // ---------------------------------------------------------------------------
 constexpr int LORA_ROWS_THREADS = 256, LORA_ROWS_CLUSTER = 8;
 
@@ -688,8 +690,9 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
 // stores took longer than a unit's bytes. 256 bytes of a row at a
 // time are what HBM wants: reading and writing 128 rows of 24 KB in place,
 // walked in pieces of 64, 128, 256 and 512 bytes, runs at 4.2, 4.6, 5.2 and
-// 5.3 TB/s. The copies of Y and V start before the kernel that makes H has
-// ended (programmatic dependent launch); only the readers of H wait for it.
+// 5.3 TB/s; 16640 rows of 12288 at rank 64 take 155 us, 5.3 TB/s. The copies
+// of Y and V start before the kernel that makes H has ended (programmatic
+// dependent launch); only the readers of H wait for it.
 //   VEC false: rows of Y that are not multiples of 16 bytes. A row's piece
 // then lies `shift` bytes into its 17 aligned 16-byte chunks, in shared memory
 // as in global memory, so that the copies in stay whole chunks; on the way out
@@ -1094,10 +1097,11 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
 // tile fastest and are cut into one equal range per CTA. The tile of X is the
 // A operand and the parts of G the B operand, both MN-major as they lie in
 // memory (one 128-byte row per step of the contraction), so nothing is
-// transposed. Sums stay in TMEM over the tiles of an adapter. An adapter
-// whose tiles are cut between CTAs leaves fp32 partial sums, slot 0 for a
-// CTA's first segment if it began before, slot 1 for the last one, and
-// k_lora_wgrad_join adds them in CTA order.
+// transposed. Sums stay in TMEM over the tiles of an adapter. An adapter whose
+// tiles are cut between CTAs leaves fp32 partial sums, slot 0 for a CTA's
+// first segment if it began before, slot 1 for the last one, and
+// k_lora_wgrad_join adds them in CTA order. 8191 rows, 4096 and 12288 columns,
+// rank 64: 59 us, 4.5 TB/s of X and dY (the join 9).
 // bf16 only: G's parts need fp32's exponent range (a power of two per row, as
 // k_lora_expand takes out, does not leave a sum over rows).
 // ---------------------------------------------------------------------------

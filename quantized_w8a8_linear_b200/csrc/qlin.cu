@@ -1394,6 +1394,21 @@ qlin_status launch_dependent(void (*kern)(P...), const char* what, dim3 grid, in
   return check_cuda(cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...), what);
 }
 
+// CTAs of `threads` threads an SM holds, asked once per device and CTA size
+// (the query is a microsecond of a nine-microsecond call).
+template <typename Kern>
+qlin_status resident_ctas(Kern kern, int threads, int smem, std::atomic<int> (&known)[16][NORM_MAX_THREADS / 32 + 1], int* per_sm) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool keep = dev >= 0 && dev < 16;
+  *per_sm = keep ? known[dev][threads / 32].load(std::memory_order_relaxed) : 0;
+  if (*per_sm > 0) return QLIN_OK;
+  QLIN_TRY(check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kern, threads, static_cast<size_t>(smem)), "cudaOccupancyMaxActiveBlocksPerMultiprocessor"));
+  if (*per_sm < 1) return fail(QLIN_ERR_UNSUPPORTED, "layer norm does not fit on an SM");
+  if (keep) known[dev][threads / 32].store(*per_sm, std::memory_order_relaxed);
+  return QLIN_OK;
+}
+
 template <typename T, int V, int OUT>
 qlin_status launch_norm_fwd_v(const NormArgs& a, int threads, int sms, cudaStream_t st) {
   auto kern = k_norm_fwd<T, V, OUT>;
@@ -1401,10 +1416,9 @@ qlin_status launch_norm_fwd_v(const NormArgs& a, int threads, int sms, cudaStrea
   static std::atomic<bool> set[16] = {};
   qlin_status s = allow_smem(kern, NORM_STAGES * V * NORM_MAX_THREADS * 16, set);
   if (s != QLIN_OK) return s;
+  static std::atomic<int> known[16][NORM_MAX_THREADS / 32 + 1] = {};
   int per_sm = 0;
-  s = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem), "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-  if (s != QLIN_OK) return s;
-  if (per_sm < 1) return fail(QLIN_ERR_UNSUPPORTED, "layer norm does not fit on an SM");
+  QLIN_TRY(resident_ctas(kern, threads, smem, known, &per_sm));
   const int64_t grid = std::min<int64_t>(a.M, static_cast<int64_t>(per_sm) * sms);
   kern<<<static_cast<unsigned>(grid), threads, smem, st>>>(a);
   return check_cuda(cudaGetLastError(), "k_norm_fwd launch");
@@ -1436,10 +1450,9 @@ qlin_status launch_norm_bwd_v(NormBwdArgs a, int threads, int groups, int sms, i
   static std::atomic<bool> set[16] = {};
   qlin_status s = allow_smem(kern, NORM_STAGES * 2 * V * MAXT * 16, set);
   if (s != QLIN_OK) return s;
+  static std::atomic<int> known[16][NORM_MAX_THREADS / 32 + 1] = {};
   int per_sm = 0;
-  s = check_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem), "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
-  if (s != QLIN_OK) return s;
-  if (per_sm < 1) return fail(QLIN_ERR_UNSUPPORTED, "layer norm's backward pass does not fit on an SM");
+  QLIN_TRY(resident_ctas(kern, threads, smem, known, &per_sm));
   ctas = std::min<int64_t>(std::min<int64_t>((a.M + groups - 1) / groups, static_cast<int64_t>(per_sm) * sms), norm_bwd_ctas(a.K));
   a.row_threads = threads / groups;
   kern<<<static_cast<unsigned>(ctas), threads, smem, st>>>(a);
