@@ -327,13 +327,17 @@ QLIN_API size_t qlin_lora_plan_bytes(int64_t M, int64_t L);
 QLIN_API qlin_status qlin_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t plan_bytes,
                            void *stream);
 
+/* Bytes of H that qlin_lora_forward needs as scratch: 4 M R, or 0 for the few
+ * rows that go through one kernel (then H may be NULL). Host-only. */
+QLIN_API size_t qlin_lora_forward_h_bytes(int64_t M, int64_t R);
+
 /* Adapters of many requests beside a shared projection, added in place to what
  * any of the linears wrote:
  *   H[i] = X[i] A[a]^T (fp32), Y[i] = xdt(Y[i] + scale[a] * H[i] B[a]^T), a = idx[i]
  * A [L,R,K] and B [L,N,R] in xdt, scale fp32 [L], all R alike (shorter
  * adapters are padded with zeros). Rows without an adapter keep their Y, bit
- * for bit. H [M,R] fp32 is written for rows that have one (kept for the
- * backward pass, else scratch). H enters the second product as two 16-bit
+ * for bit. H [M,R] fp32 is written for rows that have one: kept for the
+ * backward pass, else scratch, or NULL where qlin_lora_forward_h_bytes is 0. H enters the second product as two 16-bit
  * parts (16 significant bits in bf16, 22 in fp16); all sums are fp32 and Y is
  * rounded once. R % 8 == 0, 8 <= R <= 128; N is arbitrary up to 2^28. A row's result does
  * not depend on the other rows of the batch beyond the order in which its K

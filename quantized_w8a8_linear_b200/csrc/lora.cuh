@@ -318,7 +318,7 @@ struct LoraRowsParams {
   const uint16_t* A;    // [L,R,K]
   const uint16_t* B;    // [L,N,R]
   const float* scale;   // [L]
-  float* H;             // [M,R]
+  float* H;             // [M,R], or nullptr: not kept
   uint16_t* Y;          // [M,N]
 };
 
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(LORA_ROWS_THREADS, 2) k_lora_rows(const LoraRo
     }
     *reinterpret_cast<float4*>(sum + e) = t;
     const int j = e / R;
-    if (rank == 0 && j < n) *reinterpret_cast<float4*>(p.H + static_cast<int64_t>(oct[4 + j]) * R + e % R) = t;
+    if (rank == 0 && j < n && p.H != nullptr) *reinterpret_cast<float4*>(p.H + static_cast<int64_t>(oct[4 + j]) * R + e % R) = t;
   }
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");   // this CTA has read its peers' partial sums
   __syncthreads();

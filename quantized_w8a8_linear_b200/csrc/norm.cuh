@@ -84,8 +84,8 @@ __device__ __forceinline__ f32x2 twice(float v) { return f32x2_of(__float_as_uin
 // One row at a time per CTA, V 16-byte vectors of it per thread; the CTAs
 // stride over the rows. gamma and beta stay in registers (widened up to two
 // vectors a thread, as they are up to four).
-template <typename T, int V, int OUT>
-__global__ void __launch_bounds__(NORM_MAX_THREADS) k_norm_fwd(const NormArgs a) {
+template <typename T, int V, int OUT, int MAXT>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_fwd(const NormArgs a) {
   extern __shared__ uint4 norm_ring[];   // [NORM_STAGES][V][threads]
   __shared__ float red[2][16];
   constexpr bool WIDE = V <= 2, HOLD = V <= 4;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs
   if constexpr (COLS) {
     float* p = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.K;
     float* mine = p;
-    if (groups > 1) {   // the ring's memory, when every warp is done with it: [groups][2][K], which 3072 V bytes a warp hold up to K = 384 V
+    if (groups > 1) {   // the ring's memory, when every warp is done with it: [groups][2][K], which a warp's 96 V vectors a lane hold up to K = 384 V
       __syncthreads();
       mine = reinterpret_cast<float*>(norm_ring) + static_cast<int64_t>(group) * 2 * a.K;
     }

@@ -1409,12 +1409,12 @@ qlin_status resident_ctas(Kern kern, int threads, int smem, std::atomic<int> (&k
   return QLIN_OK;
 }
 
-template <typename T, int V, int OUT>
+template <typename T, int V, int OUT, int MAXT>
 qlin_status launch_norm_fwd_v(const NormArgs& a, int threads, int sms, cudaStream_t st) {
-  auto kern = k_norm_fwd<T, V, OUT>;
+  auto kern = k_norm_fwd<T, V, OUT, MAXT>;
   const int smem = NORM_STAGES * V * threads * 16;
   static std::atomic<bool> set[16] = {};
-  qlin_status s = allow_smem(kern, NORM_STAGES * V * NORM_MAX_THREADS * 16, set);
+  qlin_status s = allow_smem(kern, NORM_STAGES * V * MAXT * 16, set);
   if (s != QLIN_OK) return s;
   static std::atomic<int> known[16][NORM_MAX_THREADS / 32 + 1] = {};
   int per_sm = 0;
@@ -1430,17 +1430,17 @@ qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   qlin_status s = device_info(&d);
   if (s != QLIN_OK) return s;
   const int64_t KV = a.K / 8;
-  // four vectors of a row per thread while there are rows for every SM to
-  // overlap, one when a row's latency counts (and 16 warps a row at most):
-  // 16640 rows of 4096 took 41 us with four, 52 with two, 44 with eight
-  const int64_t want = a.M >= 4 * d->sms ? 4 : 1;
-  const int64_t warps = std::min<int64_t>(std::max<int64_t>((KV + 32 * want - 1) / (32 * want), 1), NORM_MAX_THREADS / 32);
+  // four vectors of a row a thread, eight where 16 warps do not hold it: 16640
+  // rows of 4096 took 41 us with four, 52 with two, 44 with eight, and 64 rows
+  // as long with four as with one (2.5 us)
+  const int64_t warps = std::min<int64_t>((KV + 127) / 128, NORM_MAX_THREADS / 32);
   const int64_t per = (KV + 32 * warps - 1) / (32 * warps);
   const int threads = static_cast<int>(32 * warps);
-  if (per <= 1) return launch_norm_fwd_v<T, 1, OUT>(a, threads, d->sms, st);
-  if (per <= 2) return launch_norm_fwd_v<T, 2, OUT>(a, threads, d->sms, st);
-  if (per <= 4) return launch_norm_fwd_v<T, 4, OUT>(a, threads, d->sms, st);
-  return launch_norm_fwd_v<T, 8, OUT>(a, threads, d->sms, st);
+  if (per <= 1) return launch_norm_fwd_v<T, 1, OUT, 256>(a, threads, d->sms, st);   // K <= 256
+  if (per <= 2) return launch_norm_fwd_v<T, 2, OUT, 256>(a, threads, d->sms, st);   // K <= 512
+  if (per <= 4 && threads <= 256) return launch_norm_fwd_v<T, 4, OUT, 256>(a, threads, d->sms, st);
+  if (per <= 4) return launch_norm_fwd_v<T, 4, OUT, 512>(a, threads, d->sms, st);
+  return launch_norm_fwd_v<T, 8, OUT, 512>(a, threads, d->sms, st);
 }
 
 template <typename T, int V, bool COLS, int MAXT>
@@ -1763,12 +1763,13 @@ qlin_status qlin_lora_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t 
   QLIN_TRY(check_common(X, xdt, M, K, N));
   if (M == 0 || N == 0) return ok();
   QLIN_TRY(check_lora(M, L, R, N, A, B, scale, plan, plan_bytes));
-  QLIN_REQ_PTR(H, "H");
+  const bool by_rows = lora_by_rows(M, R);
+  if (H != nullptr || !by_rows) QLIN_REQ_PTR(H, "H");
   QLIN_REQ_PTR(Y, "Y");
   DeviceInfo* d;
   QLIN_TRY(device_info(&d));
   const LoraCall c{M, L, R, static_cast<const int*>(plan), scale, d, static_cast<cudaStream_t>(stream)};
-  if (lora_by_rows(M, R)) {
+  if (by_rows) {
     QLIN_TRY(xdt == QLIN_BF16 ? launch_lora_rows<__nv_bfloat16>(c, X, K, A, B, N, H, Y) : launch_lora_rows<__half>(c, X, K, A, B, N, H, Y));
   } else if (xdt == QLIN_BF16) {
     QLIN_TRY((launch_lora_shrink<__nv_bfloat16, false>(c, X, K, A, nullptr, H)));
@@ -1778,6 +1779,11 @@ qlin_status qlin_lora_forward(const void* X, qlin_dtype xdt, int64_t M, int64_t 
     QLIN_TRY((launch_lora_expand<__half, false>(c, H, B, N, scale, Y)));
   }
   return ok();
+}
+
+size_t qlin_lora_forward_h_bytes(int64_t M, int64_t R) {
+  if (M < 0 || R <= 0 || lora_by_rows(M, R)) return 0;
+  return static_cast<size_t>(4 * M * R);
 }
 
 size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R) {

@@ -162,6 +162,15 @@ def test_order_of_rows_does_not_matter(q):
     assert torch.equal(Y2.cpu(), Y.cpu()[p])
 
 
+@pytest.mark.parametrize("M,R", [(3, 16), (200, 16), (40, 64), (300, 8)])
+def test_h_not_kept(q, M, R):
+    c = _case(M, 256, 136, 3, R, torch.bfloat16, "tokens", 13)
+    H = torch.zeros((M, R), device="cuda")
+    kept, _, _ = _forward(q, c, H)
+    Y, _, _ = _forward(q, c)
+    assert torch.equal(Y, kept)
+
+
 def test_update_alone_and_zero_weights(q):
     # B = 0 keeps Y's bits; Y = 0 leaves the update alone
     c = _case(200, 128, 72, 2, 16, torch.bfloat16, "spans", 3)

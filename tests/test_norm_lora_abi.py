@@ -80,10 +80,16 @@ def _fwd(q, X=P, dt=1, M=4, K=64, A=P, B=P, scale=P, L=2, R=16, N=32, plan=P, H=
 
 @pytest.mark.parametrize("kw,want", [
     (dict(K=20), 3), (dict(K=32784), 2), (dict(dt=3), 1), (dict(M=-2), 1), (dict(X=ODD), 3), (dict(A=None), 1), (dict(B=ODD), 3), (dict(scale=None), 1),
-    (dict(L=0), 2), (dict(L=1025), 2), (dict(R=12), 3), (dict(R=0), 3), (dict(R=136), 2), (dict(plan=None), 1), (dict(short=4), 4), (dict(H=None), 1),
+    (dict(L=0), 2), (dict(L=1025), 2), (dict(R=12), 3), (dict(R=0), 3), (dict(R=136), 2), (dict(plan=None), 1), (dict(short=4), 4), (dict(H=None, M=500), 1),
     (dict(H=ODD), 3), (dict(Y=None), 1), (dict(N=-1), 1), (dict(N=0), 0), (dict(M=0), 0)])
 def test_lora_forward_refusals(q, kw, want):
     assert _fwd(q, **kw) == want
+
+
+def test_h_is_scratch_for_more_than_a_few_rows(q):
+    assert q.lib.qlin_lora_forward_h_bytes(4, 16) == 0 and q.lib.qlin_lora_forward_h_bytes(256, 16) == 0
+    assert q.lib.qlin_lora_forward_h_bytes(257, 16) == 4 * 257 * 16 and q.lib.qlin_lora_forward_h_bytes(8, 64) == 4 * 8 * 64
+    assert q.lib.qlin_lora_forward_h_bytes(-1, 16) == 0 and q.lib.qlin_lora_forward_h_bytes(8, 0) == 0
 
 
 def _bwd(q, dY=P, X=P, dt=1, M=4, K=64, L=2, R=16, N=32, H=P, dX=P, dA=P, dB=P, ws=P, n=None):
