@@ -1430,16 +1430,20 @@ qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   qlin_status s = device_info(&d);
   if (s != QLIN_OK) return s;
   const int64_t KV = a.K / 8;
-  // four vectors of a row a thread, eight where 16 warps do not hold it: 16640
-  // rows of 4096 took 41 us with four, 52 with two, 44 with eight, and 64 rows
-  // as long with four as with one (2.5 us)
-  const int64_t warps = std::min<int64_t>((KV + 127) / 128, NORM_MAX_THREADS / 32);
+  // four vectors of a row a thread: 16640 rows of 4096 took 41 us with four, 52
+  // with two, 44 with eight, and 64 rows as long with four as with one (2.5 us).
+  // Over 8192 more, so that two rows still share an SM: 4352 rows of 12288 took
+  // 39 us with six (256 threads), 44 with four (384, one row an SM).
+  const int64_t most = KV <= 1024 ? 4 : KV <= 1536 ? 6 : KV <= 2048 ? 8 : KV <= 3072 ? 6 : 8;
+  const int64_t warps = (KV + 32 * most - 1) / (32 * most);
   const int64_t per = (KV + 32 * warps - 1) / (32 * warps);
   const int threads = static_cast<int>(32 * warps);
   if (per <= 1) return launch_norm_fwd_v<T, 1, OUT, 256>(a, threads, d->sms, st);   // K <= 256
   if (per <= 2) return launch_norm_fwd_v<T, 2, OUT, 256>(a, threads, d->sms, st);   // K <= 512
-  if (per <= 4 && threads <= 256) return launch_norm_fwd_v<T, 4, OUT, 256>(a, threads, d->sms, st);
-  if (per <= 4) return launch_norm_fwd_v<T, 4, OUT, 512>(a, threads, d->sms, st);
+  if (per <= 4) return launch_norm_fwd_v<T, 4, OUT, 256>(a, threads, d->sms, st);   // K <= 8192
+  if (per <= 6 && threads <= 256) return launch_norm_fwd_v<T, 6, OUT, 256>(a, threads, d->sms, st);
+  if (threads <= 256) return launch_norm_fwd_v<T, 8, OUT, 256>(a, threads, d->sms, st);
+  if (per <= 6) return launch_norm_fwd_v<T, 6, OUT, 512>(a, threads, d->sms, st);
   return launch_norm_fwd_v<T, 8, OUT, 512>(a, threads, d->sms, st);
 }
 

@@ -27,7 +27,7 @@ pytestmark = pytest.mark.gpu
 
 U, D = 2.0 ** -24, 80
 SHAPES = [(1, 16), (1, 4096), (3, 48), (13, 1040), (37, 4096), (5, 8192), (600, 528), (700, 2064), (2, 32768), (9, 12288),
-          (640, 4096), (650, 12304), (620, 32768), (1500, 16)]
+          (640, 4096), (650, 12304), (620, 32768), (1500, 16), (300, 8208), (5, 16384), (7, 16400), (4, 24576), (3, 24592)]
 
 
 @pytest.fixture(scope="module")
