@@ -778,8 +778,8 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
   const int64_t units = static_cast<int64_t>(p.plan.tiles()) * nbs;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   const int t0 = static_cast<int>(u0 / nbs), nb0 = static_cast<int>(u0 % nbs);   // first tile and columns
-  // byte of its aligned 16-byte chunk at which the piece of `row` from column n0 starts
-  auto shift_of = [&](int64_t row, int64_t n0) { return VEC ? 0 : static_cast<int>((2 * (row * p.N + n0)) & 15); };
+  // byte of its aligned 16-byte chunk at which `row`, and any piece of it, starts (a unit's columns are 256 bytes)
+  auto shift_of = [&](int row) { return VEC ? 0 : static_cast<int>((2u * static_cast<uint32_t>(row) * static_cast<uint32_t>(p.N)) & 15u); };
 
   if (warp < 4) {
     // ---------------- copies of Y: chunk c of rows r0, r0 + 8, ..., 16 lanes a row ----------------
@@ -787,28 +787,40 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     const int64_t all = 2 * p.plan.M * p.N;   // bytes of Y
     const int row_size = static_cast<int>(2 * p.N), M = static_cast<int>(p.plan.M);
     const uint8_t* Y = reinterpret_cast<const uint8_t*>(p.Y);
-    int rows[16];
+    // a row's first aligned chunk, its shift in the low bits; -1 past the count
+    int64_t row_at[16];
     int stage = 0;
     uint32_t phase = 0;
     bool good = true, next = true;
     for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
       if (next) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) rows[i] = p.plan.rows(static_cast<int>(t))[r0 + 8 * i];   // M past the count
+        for (int i = 0; i < 16; ++i) {
+          const int row = p.plan.rows(static_cast<int>(t))[r0 + 8 * i];   // M past the count
+          row_at[i] = row < M ? row_bytes(row, row_size) : -1;
+        }
       }
       good = __all_sync(0xffffffffu, mbar_wait(&yempty_bar[stage], phase ^ 1u, abort_flag));
       if (!good) break;
       const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
-      const int bytes = static_cast<int>(2 * (p.N - n0 < LORA_EXPAND_BN ? p.N - n0 : LORA_EXPAND_BN));
-      const uint32_t d = smem_u32(sY(stage)) + r0 * S::Y_ROW;
+      const uint32_t d = smem_u32(sY(stage)) + r0 * S::Y_ROW + 16 * c;
+      if (nb + 2 < nbs) {   // whole units whose chunks end within the row's matrix
+        const uint8_t* y = Y + 2 * n0 + 16 * c;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (rows[i] < M) {
-          const int64_t b = row_bytes(rows[i], row_size) + 2 * n0;
-          const int shift = VEC ? 0 : static_cast<int>(b & 15);
-          const int64_t at = b - shift + 16 * c;
-          if (16 * c < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i + 16 * c, Y + at, VEC ? 16 : all - at);
-          if (!VEC && c == 0 && 256 < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i + 256, Y + at + 256, all - at - 256);
+        for (int i = 0; i < 16; ++i) {
+          if (row_at[i] >= 0) {
+            cp_async16_or_zero(d + 8 * S::Y_ROW * i, y + (VEC ? row_at[i] : row_at[i] & ~int64_t{15}), true);
+            if (!VEC && c == 0 && (row_at[i] & 15) != 0) cp_async16_or_zero(d + 8 * S::Y_ROW * i + 256, y + 256 + (row_at[i] & ~int64_t{15}), true);
+          }
+        }
+      } else {
+        const int bytes = static_cast<int>(2 * (p.N - n0 < LORA_EXPAND_BN ? p.N - n0 : LORA_EXPAND_BN));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int shift = VEC ? 0 : static_cast<int>(row_at[i] & 15);
+          const int64_t at = row_at[i] - shift + 2 * n0 + 16 * c;
+          if (row_at[i] >= 0 && 16 * c < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i, Y + at, VEC ? 16 : all - at);
+          if (!VEC && row_at[i] >= 0 && c == 0 && 256 < shift + bytes) cp_async_upto16(d + 8 * S::Y_ROW * i + 256, Y + at + 256, all - at - 256);
         }
       }
       cp_async_arrive(&yfull_bar[stage]);
@@ -964,7 +976,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
       if (n > 0) {
         const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
         uint8_t* yr = sY(stage) + q * 32 * S::Y_ROW;   // the warp's rows
-        const int shift = shift_of(my_row, n0);
+        const int shift = shift_of(my_row);
         // VEC false: the piece from the 8-byte word it starts in; `late`: it starts
         // in that word's second half; `odd`: in the upper 16 bits of a 32-bit word,
         // so that pairs of columns straddle two
@@ -1047,7 +1059,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
             if constexpr (VEC) {
               if (col + 8 * c < N) *reinterpret_cast<uint4*>(dst + 16 * c) = *reinterpret_cast<const uint4*>(src + 16 * c);
             } else {
-              const int sh = shift_of(row, n0);
+              const int sh = shift_of(row);
               const int cols = N - col < 64 ? N - col : 64;
               // with a shift, the piece has `head` elements before its first whole
               // chunk and 8 - head behind its last one: one of the eight for each lane
