@@ -82,7 +82,8 @@ constexpr int LORA_PLAN_THREADS = 1024;
 // adapters of its contiguous share of the rows, a scan over (adapter, warp)
 // turns the counts into places, and the warps walk their shares again, each
 // row's place within 32 rows from the ballot of its equals. No atomics, so
-// the order (and every sum over it) is the same in every run.
+// the order (and every sum over it) is the same in every run. 64 rows take
+// 7 us, 16640 rows 16: once a batch, beside two launches for each projection.
 __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx, int64_t M, int64_t L64, int* plan) {
   extern __shared__ int lora_count[];   // [32][L], then [L] first octets
   __shared__ int warp_total[32], warp_octets[32];
@@ -96,15 +97,27 @@ __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx,
   for (int i = tid; i < 32 * L; i += LORA_PLAN_THREADS) lora_count[i] = 0;
   __syncthreads();
   int* mine = lora_count + warp * L;
-  auto adapter = [&](int64_t m) {
-    const int a = m < hi ? idx[m] : -1;
-    return a >= 0 && a < L ? a : -1;
+  // the adapters of 256 rows from m0 on, eight loads in flight (one by one,
+  // 16640 rows took 21 us)
+  auto adapters = [&](int64_t m0, int (&a)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t m = m0 + 32 * j + lane;
+      a[j] = m < hi ? __ldg(idx + m) : -1;
+      if (a[j] >= L) a[j] = -1;
+    }
   };
-  for (int64_t m0 = lo; m0 < hi; m0 += 32) {
-    const int a = adapter(m0 + lane);
-    const uint32_t same = __match_any_sync(0xffffffffu, a);
-    if (a >= 0 && lane == __ffs(same) - 1) mine[a] += __popc(same);
-    __syncwarp();
+  for (int64_t m0 = lo; m0 < hi; m0 += 256) {
+    int as[8];
+    adapters(m0, as);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (m0 + 32 * j >= hi) break;
+      const int a = as[j];
+      const uint32_t same = __match_any_sync(0xffffffffu, a);
+      if (a >= 0 && lane == __ffs(same) - 1) mine[a] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   // thread a: rows of adapter a, and the places of its rows within them
@@ -168,18 +181,24 @@ __global__ void __launch_bounds__(LORA_PLAN_THREADS) k_lora_plan(const int* idx,
     plan[tid] = tid == 0 ? static_cast<int>(M) : tid == 1 ? L : tid == 2 ? total : tid == 3 ? ototal : 0;
   }
   __syncthreads();
-  for (int64_t m0 = lo; m0 < hi; m0 += 32) {
-    const int a = adapter(m0 + lane);
-    const uint32_t same = __match_any_sync(0xffffffffu, a);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    if (a >= 0) {
-      const int at = mine[a] + rank;
-      rows[at] = static_cast<int>(m0 + lane);
-      if (in_octets) octet[LORA_OCTET_WORDS * (first_octet[a] + at / 8) + 4 + at % 8] = static_cast<int>(m0 + lane);
+  for (int64_t m0 = lo; m0 < hi; m0 += 256) {
+    int as[8];
+    adapters(m0, as);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (m0 + 32 * j >= hi) break;
+      const int a = as[j], row = static_cast<int>(m0) + 32 * j + lane;
+      const uint32_t same = __match_any_sync(0xffffffffu, a);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      if (a >= 0) {
+        const int at = mine[a] + rank;
+        rows[at] = row;
+        if (in_octets) octet[LORA_OCTET_WORDS * (first_octet[a] + at / 8) + 4 + at % 8] = row;
+      }
+      __syncwarp();
+      if (a >= 0 && rank == 0) mine[a] += __popc(same);
+      __syncwarp();
     }
-    __syncwarp();
-    if (a >= 0 && rank == 0) mine[a] += __popc(same);
-    __syncwarp();
   }
 }
 

@@ -277,6 +277,32 @@ def test_without_dx_and_without_rows(q):
     assert not dA.any() and not dB.any()
 
 
+@pytest.mark.parametrize("M,L", [(1, 1), (31, 1024), (256, 3), (257, 3), (1000, 1000), (4352, 48), (20000, 2), (33000, 1024)])
+def test_plan_is_a_stable_sort(q, M, L):
+    g = torch.Generator().manual_seed(M + L)
+    idx = torch.randint(-2, L + 2, (M,), generator=g, dtype=torch.int32)
+    plan = q.qlin_lora_plan(idx.cuda(), L).view(torch.int32).cpu()
+    most = M // 128 + min(L, M)
+    info_at = 16 + (L + 4) // 4 * 4
+    rows_at = info_at + (2 * most + 3) // 4 * 4
+    info, rows = plan[info_at:info_at + 2 * most].view(-1, 2), plan[rows_at:rows_at + 128 * most].view(-1, 128)
+    tiles = int(plan[2])
+    assert plan[0] == M and plan[1] == L and tiles <= most and plan[16 + L] == tiles
+    on = ((idx >= 0) & (idx < L)).nonzero()[:, 0]
+    want = on[torch.sort(idx[on], stable=True).indices].int()
+    got = [rows[t][:int(info[t, 1])] for t in range(tiles)]
+    assert torch.equal(torch.cat(got) if got else want[:0], want)
+    assert all((rows[t][int(info[t, 1]):] == M).all() and (idx[got[t].long()] == info[t, 0]).all() for t in range(tiles))
+    octets = int(plan[3])
+    assert (octets > 0) == (M <= 256 and want.numel() > 0)
+    at = rows_at + 128 * most
+    o = plan[at:at + 12 * octets].view(-1, 12)
+    eights = [o[t, 4:4 + int(o[t, 1])] for t in range(octets)]
+    if octets:
+        assert torch.equal(torch.cat(eights), want)
+        assert all((o[t, 4 + int(o[t, 1]):] == M).all() and (idx[eights[t].long()] == o[t, 0]).all() for t in range(octets))
+
+
 def test_plan_of_another_batch_is_refused(q):
     c = _case(150, 128, 72, 2, 16, torch.bfloat16, "spans", 8)
     _, plan, d = _forward(q, c)
