@@ -31,6 +31,7 @@
 // All mbarrier waits are bounded (common.cuh).
 #pragma once
 #include "common.cuh"
+#include "vec.cuh"
 
 namespace qlin {
 

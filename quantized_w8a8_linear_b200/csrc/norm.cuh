@@ -15,6 +15,7 @@
 // rows in and out), backward 71 us (5.8 TB/s), its column sums another 7.
 #pragma once
 #include "common.cuh"
+#include "vec.cuh"
 
 namespace qlin {
 
