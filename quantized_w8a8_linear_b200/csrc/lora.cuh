@@ -502,9 +502,16 @@ struct LoraShrinkParams {
 // 36 with two CTAs of two stages each); else two CTAs an SM, in clusters (64
 // tiles of 12288: 47 us in clusters of four, 52 with one deep CTA in clusters
 // of two). Above rank 64 a stage is larger: three of them, one CTA.
+// ACCS accumulators take the stages in turn, as many as the CTAs of an SM have
+// TMEM for: an MMA cuts its fp32 sum off instead of rounding it, so a sum of
+// 4096 products in one chain of 256 MMAs came out 4e-6 of its size too small
+// (2.5e-5 where all are positive). Eight chains of 32, added with rounding by
+// the epilogue: 4e-7 (torch's fp32 product: 6e-7), at no measurable time.
 template <int RB, bool DEEP>
 struct LoraShrinkSmem {
   static constexpr int STAGES = RB == 2 ? 3 : DEEP ? 4 : 2;
+  static constexpr int ACC_COLS = RB * 64;
+  static constexpr int ACCS = (RB == 2 || DEEP ? 512 : 256) / ACC_COLS;
   static constexpr int A_BYTES = 2 * LORA_TILE * 128;   // two halves of 64 columns
   static constexpr int W_BYTES = 2 * RB * 64 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
   uint64_t* drain_bar = tfull_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr uint32_t TCOLS = RB * 64;
+  constexpr uint32_t TCOLS = S::ACCS * S::ACC_COLS;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -612,16 +619,29 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     const float s = p.scale != nullptr ? __ldg(p.scale + a) : 1.0f;
     float* out = cluster > 1 ? reinterpret_cast<float*>(smem) + r * (Rp + 4) : p.H + static_cast<int64_t>(r < n ? rows[r] : 0) * p.R;
     if (q * 32 < n) {
+      const int accs = kb1 - kb0 < S::ACCS ? kb1 - kb0 : S::ACCS;   // those with a sum
       for (int c0 = 0; c0 < p.R; c0 += 16) {
-        uint32_t v[16];
-        __syncwarp();
-        tmem_ld16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
-        tmem_wait16(v);
+        float sum[16] = {};
+#pragma unroll
+        for (int b0 = 0; b0 < S::ACCS; b0 += 4) {
+          uint32_t v[4][16];
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) tmem_ld16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((b0 + b) * S::ACC_COLS + c0), v[b]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            tmem_wait16(v[b]);
+            if (b0 + b < accs) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[i] += __uint_as_float(v[b][i]);
+            }
+          }
+        }
         if (r < n) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             if (c0 + i < p.R) {
-              float4 f = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+              float4 f = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
               if (!good) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               if (cluster == 1) {
                 f = make_float4(f.x * s, f.y * s, f.z * s, f.w * s);
@@ -645,17 +665,26 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
       fence_proxy_async_smem();   // X was written by cp.async, through the generic proxy
       tc_fence_after();
       const uint32_t as = smem_u32(sA(stage)), ws = smem_u32(sW(stage));
+      const uint32_t d = tmem_base + static_cast<uint32_t>((kb - kb0) % S::ACCS * S::ACC_COLS);
 #pragma unroll
       for (int k = 0; k < LORA_SHRINK_BK / 16; ++k) {
         const uint64_t adesc = sdesc_k128(as + (k >> 2) * (LORA_TILE * 128)) + 2u * (k & 3);
         const uint64_t bdesc = W_MN ? sdesc_mn128(ws, 16384u) + 128u * k : sdesc_k128(ws + (k >> 2) * (RB * 8192)) + 2u * (k & 3);
-        umma<2>(tmem_base, adesc, bdesc, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+        umma<2>(d, adesc, bdesc, idesc, (kb - kb0 >= S::ACCS || k != 0) ? 1u : 0u);
       }
       umma_commit(&empty_bar[stage]);
       if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
     }
     umma_commit(tfull_bar);
     drain_mma(drain_bar);
+  }
+  // TMEM goes back before the CTAs of a cluster wait for one another: a peer
+  // may be waiting for another kernel's on its SM
+  __syncthreads();
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TCOLS);
   }
   if (cluster > 1) {
     cluster_sync();
@@ -686,12 +715,6 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
       const int c = e % r4 * 4;
       store_split4<T>(p.Gs + row * 2 * p.R + c, p.R, *reinterpret_cast<const float4*>(p.G + row * p.R + c));
     }
-  }
-  __syncthreads();
-  if (warp == 4) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem_base, TCOLS);
   }
 }
 
