@@ -22,11 +22,16 @@
 // A few rows (a decode step) go through k_lora_rows instead, one launch for
 // both products of up to eight rows of one adapter.
 //
-// H enters the second product as two 16-bit parts, hi = T(h) and
-// lo = T(h - hi), two MMAs on one staged operand: 16 (bf16) or 22 (fp16)
-// significant bits, where hi alone would add an error of the size of the
-// output's own rounding. fp16 parts are taken of h / 2^e with 2^e the largest
-// power of two in the row (exact), so neither overflow nor subnormals cut them.
+// H enters the second product as three 16-bit parts, T(h), T of what that
+// leaves and T of what both leave, three MMAs on one staged operand: fp32's 24
+// bits, so that a row comes out the same as where H stays fp32 (k_lora_rows).
+// With two parts, 16 bits in bf16, 2^-17 of the update showed in Y where it
+// cancels, and more of Y's elements than an fp32 product has rounded the other
+// way; the third one costs 1 to 5% (16640 x 4096 -> 12288, rank 64: 198 us in
+// all, 190 with two). The smallest go first, while the accumulator is small. fp16
+// parts are taken of h 2^14 / 2^e with 2^e the largest power of two in the row
+// (exact): nothing overflows, all 24 bits of what is above 2^-15 of the row's
+// largest are kept, and of the rest all above 2^-39 of it.
 //
 // All mbarrier waits are bounded (common.cuh).
 #pragma once
@@ -289,30 +294,33 @@ __device__ __forceinline__ void drain_mma(uint64_t* bar) {
   while (!mbar_try_wait(a, 0) && globaltimer() - t0 < drain_limit_ns()) {}
 }
 
-// 8 fp32 values -> two 16-byte chunks of 16-bit values, hi + lo = the value to
-// 16 (bf16) or 22 (fp16) bits. Where hi is not finite lo is 0, so an infinite
-// or NaN value stays what it is.
+// 8 fp32 values -> three 16-byte chunks of 16-bit values whose sum is the
+// value. Where the first is not finite the others are 0, so an infinite or NaN
+// value stays what it is.
 template <typename T>
-__device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo) {
-  uint16_t h[8], l[8];
+__device__ __forceinline__ void split8(const float (&f)[8], uint4 (&part)[3]) {
+  uint16_t h[3][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    h[i] = from_f<T>(f[i]);
-    const float r = f[i] - to_f<T>(h[i]);
-    l[i] = fabsf(r) <= fabsf(f[i]) ? from_f<T>(r) : static_cast<uint16_t>(0);   // false for NaN and for hi = inf
+    h[0][i] = from_f<T>(f[i]);
+    float r = f[i] - to_f<T>(h[0][i]);
+    r = fabsf(r) <= fabsf(f[i]) ? r : 0.0f;   // false for NaN and for an infinite first part
+    h[1][i] = from_f<T>(r);
+    h[2][i] = from_f<T>(r - to_f<T>(h[1][i]));
   }
-  hi = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
-  lo = make_uint4(l[0] | (l[1] << 16), l[2] | (l[3] << 16), l[4] | (l[5] << 16), l[6] | (l[7] << 16));
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    part[j] = make_uint4(h[j][0] | (h[j][1] << 16), h[j][2] | (h[j][3] << 16), h[j][4] | (h[j][5] << 16), h[j][6] | (h[j][7] << 16));
 }
 
 // The same for 4 values, written to row[0] and row[R] of a split row [2][R].
 template <typename T>
 __device__ __forceinline__ void store_split4(uint16_t* row, int R, const float4& v) {
   const float f[8] = {v.x, v.y, v.z, v.w};
-  uint4 hi, lo;
-  split8<T>(f, hi, lo);
-  *reinterpret_cast<uint2*>(row) = make_uint2(hi.x, hi.y);
-  *reinterpret_cast<uint2*>(row + R) = make_uint2(lo.x, lo.y);
+  uint4 part[3];
+  split8<T>(f, part);
+  *reinterpret_cast<uint2*>(row) = make_uint2(part[0].x, part[0].y);
+  *reinterpret_cast<uint2*>(row + R) = make_uint2(part[1].x, part[1].y);
 }
 
 // ---------------------------------------------------------------------------
@@ -719,7 +727,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
 }
 
 // ---------------------------------------------------------------------------
-// k_lora_expand: Y[rows of the tile] += s (hi + lo) V^T, 128 columns a unit.
+// k_lora_expand: Y[rows of the tile] += s H V^T, 128 columns a unit, H in parts.
 //   V_MN 0: V = B[a] [N, R], K-major;   1: V = A[a] [R, K] read as its
 //   transpose, MN-major, with Y = dX and K columns.
 // Persistent, one CTA an SM: the units (tile, 128 columns), columns fastest,
@@ -755,14 +763,14 @@ struct LoraExpandParams {
 
 template <int RB>
 struct LoraExpandSmem {
-  static constexpr int V_STAGES = 2;
+  static constexpr int V_STAGES = RB == 1 ? 2 : 3;                     // each 64 of R
   static constexpr int Y_STAGES = RB == 1 ? 4 : 2;
   static constexpr int H_BYTES = RB * LORA_TILE * 128;                 // one part
-  static constexpr int V_BYTES = RB * LORA_EXPAND_BN * 128;
+  static constexpr int V_BYTES = LORA_EXPAND_BN * 128;
   static constexpr int Y_ROW = 272;
   static constexpr int Y_BYTES = LORA_TILE * Y_ROW;
   static constexpr int BAR_BYTES = 8 * (2 * V_STAGES + 2 * Y_STAGES + 7) + 16;
-  static constexpr int TOTAL = 1024 + 2 * H_BYTES + V_STAGES * V_BYTES + Y_STAGES * Y_BYTES + BAR_BYTES;
+  static constexpr int TOTAL = 1024 + 3 * H_BYTES + V_STAGES * V_BYTES + Y_STAGES * Y_BYTES + BAR_BYTES;
   static_assert(TOTAL <= 227 * 1024, "k_lora_expand shared memory");
 };
 
@@ -771,10 +779,10 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
   using S = LoraExpandSmem<RB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sH = smem;   // [hi, lo][RB][128 rows][128 bytes]
-  auto sV = [&](int s) { return smem + 2 * S::H_BYTES + s * S::V_BYTES; };
-  auto sY = [&](int s) { return smem + 2 * S::H_BYTES + S::V_STAGES * S::V_BYTES + s * S::Y_BYTES; };
-  uint64_t* vfull_bar = reinterpret_cast<uint64_t*>(smem + 2 * S::H_BYTES + S::V_STAGES * S::V_BYTES + S::Y_STAGES * S::Y_BYTES);
+  uint8_t* sH = smem;   // [3 parts][RB][128 rows][128 bytes]
+  auto sV = [&](int s) { return smem + 3 * S::H_BYTES + s * S::V_BYTES; };
+  auto sY = [&](int s) { return smem + 3 * S::H_BYTES + S::V_STAGES * S::V_BYTES + s * S::Y_BYTES; };
+  uint64_t* vfull_bar = reinterpret_cast<uint64_t*>(smem + 3 * S::H_BYTES + S::V_STAGES * S::V_BYTES + S::Y_STAGES * S::Y_BYTES);
   uint64_t* vempty_bar = vfull_bar + S::V_STAGES;
   uint64_t* yfull_bar = vempty_bar + S::V_STAGES;
   uint64_t* yempty_bar = yfull_bar + S::Y_STAGES;
@@ -885,18 +893,20 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
       int a = u0 < u1 ? p.plan.info(t0).x : 0;
       for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
         const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
-        good = mbar_wait(&vempty_bar[stage], phase ^ 1u, abort_flag);
-        if (!good) break;
-        mbar_arrive_expect_tx(&vfull_bar[stage], S::V_BYTES);
-        if constexpr (V_MN) {
+        for (int b = 0; b < RB; ++b) {   // 64 of R a stage
+          good = mbar_wait(&vempty_bar[stage], phase ^ 1u, abort_flag);
+          if (!good) break;
+          mbar_arrive_expect_tx(&vfull_bar[stage], S::V_BYTES);
+          if constexpr (V_MN) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) tma_load_3d(sV(stage) + h * (RB * 64 * 128), &tmV, &vfull_bar[stage], n0 + 64 * h, 0, a);
-        } else {
-#pragma unroll
-          for (int b = 0; b < RB; ++b) tma_load_3d(sV(stage) + b * (LORA_EXPAND_BN * 128), &tmV, &vfull_bar[stage], b * 64, n0, a);
+            for (int h = 0; h < 2; ++h) tma_load_3d(sV(stage) + h * 8192, &tmV, &vfull_bar[stage], n0 + 64 * h, b * 64, a);
+          } else {
+            tma_load_3d(sV(stage), &tmV, &vfull_bar[stage], b * 64, n0, a);
+          }
+          issued |= 1u << stage;
+          if (++stage == S::V_STAGES) { stage = 0; phase ^= 1u; }
         }
-        issued |= 1u << stage;
-        if (++stage == S::V_STAGES) { stage = 0; phase ^= 1u; }
+        if (!good) break;
         if (++nb == nbs) {
           nb = 0;
           if (u + 1 < u1) a = p.plan.info(static_cast<int>(++t)).x;
@@ -908,7 +918,6 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16(LORA_TILE, LORA_EXPAND_BN, std::is_same<T, __nv_bfloat16>::value) | (V_MN ? IDESC_B_MN : 0u);
-      constexpr int KS = 4 * RB;
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, h_phase = 0;
       bool next = true;
@@ -918,20 +927,25 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
           h_phase ^= 1u;
         }
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag)) break;
-        if (!mbar_wait(&vfull_bar[stage], phase, abort_flag)) break;
-        tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * LORA_EXPAND_BN);
-        const uint32_t v = smem_u32(sV(stage)), h = smem_u32(sH);
+        bool good = true;
+        for (int b = 0; b < RB; ++b) {   // 64 of R
+          good = mbar_wait(&vfull_bar[stage], phase, abort_flag);
+          if (!good) break;
+          tc_fence_after();
+          const uint32_t v = smem_u32(sV(stage)), h = smem_u32(sH) + static_cast<uint32_t>(b * (LORA_TILE * 128));
 #pragma unroll
-        for (int k = 0; k < 2 * KS; ++k) {   // both parts of H; zeros past R
-          const int i = k % KS;
-          const uint64_t adesc = sdesc_k128(h + (k / KS) * S::H_BYTES + (i >> 2) * (LORA_TILE * 128)) + 2u * (i & 3);
-          const uint64_t bdesc = V_MN ? sdesc_mn128(v, KS * 2048u) + 128u * i : sdesc_k128(v + (i >> 2) * (LORA_EXPAND_BN * 128)) + 2u * (i & 3);
-          umma<2>(d, adesc, bdesc, idesc, k != 0 ? 1u : 0u);
+          for (int k = 0; k < 12; ++k) {   // the smallest part of H first; zeros past R
+            const int i = k & 3, part = 2 - (k >> 2);
+            const uint64_t adesc = sdesc_k128(h + part * S::H_BYTES) + 2u * i;
+            const uint64_t bdesc = V_MN ? sdesc_mn128(v, 8192u) + 128u * i : sdesc_k128(v) + 2u * i;
+            umma<2>(d, adesc, bdesc, idesc, k != 0 || b != 0 ? 1u : 0u);
+          }
+          umma_commit(&vempty_bar[stage]);
+          if (++stage == S::V_STAGES) { stage = 0; phase ^= 1u; }
         }
-        umma_commit(&vempty_bar[stage]);
+        if (!good) break;
         umma_commit(&tfull_bar[acc]);
-        if (++stage == S::V_STAGES) { stage = 0; phase ^= 1u; }
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         next = ++nb == nbs;
         if (next) {
@@ -987,11 +1001,10 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
             for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
 #pragma unroll
             for (int o = CH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            // 2^e <= max < 2^(e+1); rows of zeros, subnormals, infinities keep 1
-            const uint32_t eb = __float_as_uint(m) >> 23;
-            const bool norm = eb >= 1 && eb <= 253;
-            const float up = norm ? __uint_as_float(eb << 23) : 1.0f;
-            const float down = norm ? __uint_as_float((254u - eb) << 23) : 1.0f;
+            // up = 2^(e - 14) with 2^e <= max < 2^(e+1), down = 1 / up; rows with infinities or NaN keep 1
+            const uint32_t em = __float_as_uint(m) >> 23, eb = em > 15u ? em - 14u : 1u;
+            const float up = em < 255u ? __uint_as_float(eb << 23) : 1.0f;
+            const float down = em < 255u ? __uint_as_float((254u - eb) << 23) : 1.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= down;
             // the lane whose TMEM row this is keeps 2^e: rows of this step are r of lanes 0, CH, ...
@@ -999,12 +1012,12 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
             if (lane / (32 / CH) == i) s = sa * up_mine;
           }
           if (mine) {
-            uint4 hi, lo;
-            split8<T>(f, hi, lo);
+            uint4 part[3];
+            split8<T>(f, part);
             const int rr = q * 32 + r;
             uint8_t* h = sH + (c >> 3) * (LORA_TILE * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-            *reinterpret_cast<uint4*>(h) = hi;
-            *reinterpret_cast<uint4*>(h + S::H_BYTES) = lo;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(h + j * S::H_BYTES) = part[j];
           }
         }
         fence_proxy_async_smem();

@@ -1668,7 +1668,7 @@ qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, cons
 template <typename T, int RB, bool V_MN, bool VEC>
 qlin_status launch_lora_expand_rb(const LoraCall& c, const float* H, const void* V, int64_t N, const float* scale, void* Y) {
   CUtensorMap tv;
-  if (V_MN) QLIN_TRY(make_tmap_adapters(&tv, V, c.L, c.R, N, RB * 64));
+  if (V_MN) QLIN_TRY(make_tmap_adapters(&tv, V, c.L, c.R, N, 64));
   else QLIN_TRY(make_tmap_adapters(&tv, V, c.L, N, c.R, LORA_EXPAND_BN));
   auto kern = k_lora_expand<T, RB, V_MN, VEC>;
   constexpr int smem = LoraExpandSmem<RB>::TOTAL;

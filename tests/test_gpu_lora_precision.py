@@ -44,3 +44,62 @@ def test_h_is_summed_in_short_chains(q, M, R, chain, dtype):
     # the chains' sums, then at most eight of them (four, and the parts of eight CTAs) added with a rounding each
     tol = 4 * (chain + 1) / 2 * 2.0 ** -23 + 11 * 2.0 ** -24
     assert ((H.double() - h).abs() / h).max().item() <= tol
+
+
+def _ladder(g, L, R, C, dtype):
+    """[L,R,C] positive, row r 4^-r the size of row 0: the largest and the smallest of a row of H are 2^14 apart."""
+    return (16.0 * 4.0 ** -torch.arange(R, device="cuda")[:, None] * (0.5 + torch.rand((L, R, C), generator=g, device="cuda"))).to(dtype)
+
+
+def _pick(g, L, R, C, dtype):
+    """[L,C,R] with one positive weight a column: column c reads element c % R of H alone."""
+    b = torch.zeros((L, C, R), device="cuda")
+    c = torch.arange(C, device="cuda")
+    b[:, c, c % R] = 0.5 + torch.rand((L, C), generator=g, device="cuda")
+    return b.to(dtype)
+
+
+def _check_difference(got, base, update, dtype):
+    """got = T(base + update), where base = -T(update): what is left is as small as the roundings of `update`. Two
+    MMAs in line lose four steps each of their sums (16 products, then H's largest part's one; the smaller parts'
+    sums are 2^-8 of that at most, and their losses less than another step), and the last addition rounds once."""
+    want = base.double() + update
+    e = (4 + 4 + 1) * 2.0 ** -23 * update.abs()
+    tol = e + torch.finfo(dtype).eps / 2 * (want.abs() + e) + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M,R", [(200, 8), (300, 8), (300, 72)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_y_sees_all_bits_of_h(q, M, R, dtype):
+    # 16 products, one MMA, for each element of H: what is left of Y + update - T(update) shows how exactly H entered.
+    # 200 rows of rank 8 go through the kernel of few rows, in the batch of 300 through the tiles'
+    K, N, L = 16, 520, 3
+    g = torch.Generator(device="cuda").manual_seed(M + R)
+    X, A, B = _positive(g, (M, K), dtype), torch.zeros((L, R, K), dtype=dtype, device="cuda"), torch.zeros((L, N, R), dtype=dtype, device="cuda")
+    A[:, -8:], B[:, :, -8:] = _ladder(g, L, 8, K, dtype), _pick(g, L, 8, N, dtype)
+    idx = (torch.arange(M, device="cuda") % L).to(torch.int32)
+    scale = 0.5 + torch.rand(L, generator=g, device="cuda")
+    update = torch.zeros((M, N), dtype=torch.float64, device="cuda")
+    for a in range(L):
+        update[idx == a] = scale[a].double() * (X[idx == a].double() @ A[a].double().T @ B[a].double().T)
+    base = -update.to(dtype)
+    Y = q.qlin_lora_forward(X, A, B, scale, q.qlin_lora_plan(idx, L), base.clone())
+    _check_difference(Y, base, update, dtype)
+
+
+@pytest.mark.parametrize("R", [8, 72])
+def test_dx_sees_all_bits_of_dh(q, R):
+    dtype, M, K, N, L = torch.bfloat16, 300, 528, 16, 3
+    g = torch.Generator(device="cuda").manual_seed(R)
+    X, dY = _positive(g, (M, K), dtype), _positive(g, (M, N), dtype)
+    A, B = torch.zeros((L, R, K), dtype=dtype, device="cuda"), torch.zeros((L, N, R), dtype=dtype, device="cuda")
+    A[:, -8:], B[:, :, -8:] = _pick(g, L, 8, K, dtype).transpose(1, 2), _ladder(g, L, 8, N, dtype).transpose(1, 2)
+    idx = (torch.arange(M, device="cuda") % L).to(torch.int32)
+    scale = 0.5 + torch.rand(L, generator=g, device="cuda")
+    update = torch.zeros((M, K), dtype=torch.float64, device="cuda")
+    for a in range(L):
+        update[idx == a] = scale[a].double() * (dY[idx == a].double() @ B[a].double() @ A[a].double())
+    base = -update.to(dtype)
+    dX, _, _ = q.qlin_lora_backward(dY, X, A, B, scale, q.qlin_lora_plan(idx, L), torch.zeros((M, R), device="cuda"), dX=base.clone())
+    _check_difference(dX, base, update, dtype)
