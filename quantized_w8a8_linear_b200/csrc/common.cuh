@@ -21,8 +21,8 @@ namespace qlin {
 __device__ int g_status = 0;
 __device__ unsigned long long g_wait_timeout_ns = 2000000000ull;
 // Test switch of the abort path (off unless qlin_debug_inject_wait_timeout
-// sets it): the GEMM's MMA warp first waits on a barrier that nothing
-// arrives on, so that its bounded wait runs out.
+// sets it): the MMA warp of k_gemm and of the adapters' tile kernels first
+// waits on a barrier that nothing arrives on, so that its bounded wait runs out.
 __device__ int g_inject_wait_timeout = 0;
 
 __device__ __forceinline__ uint64_t globaltimer() {
@@ -110,6 +110,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
+}
+
+// The same for a whole warp, with one answer for all its lanes. Each lane has
+// its own deadline, so at the limit some may give up while others are let
+// through; a warp that goes on to collective instructions (__syncwarp,
+// tcgen05.ld) has to go on or stop as one.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
 // Barrier among a group of threads on an mbarrier whose arrival count is the

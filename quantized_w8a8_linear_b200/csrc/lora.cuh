@@ -273,8 +273,9 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-// Waits (bounded) for the copies a producer that gave up still has in flight:
-// the ring slots before `stage` in issue order, as far as they were used.
+// Waits (bounded) for the last copies of a producer, in the ring slots before
+// `stage` in issue order as far as they were used: whoever reads them may have
+// given up, and the CTA must not end before they have landed.
 __device__ __forceinline__ void drain_ring(uint64_t* full_bar, int stages, int stage, uint32_t phase, uint32_t issued) {
   for (int i = 0; i < stages; ++i) {
     if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
@@ -284,6 +285,12 @@ __device__ __forceinline__ void drain_ring(uint64_t* full_bar, int stages, int s
       while (!mbar_try_wait(a, phase) && globaltimer() - t0 < drain_limit_ns()) {}
     }
   }
+}
+
+// Test of the abort path (qlin_debug_inject_wait_timeout): nothing has
+// committed to the MMA thread's drain barrier yet, so this wait runs out.
+__device__ __forceinline__ bool injected_wait(uint64_t* drain_bar, volatile int* abort_flag) {
+  return g_inject_wait_timeout == 0 || mbar_wait(drain_bar, 0, abort_flag);
 }
 
 // Waits (bounded) for the MMAs this thread issued, before TMEM is freed.
@@ -594,7 +601,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     uint32_t phase = 0, issued = 0;
     bool good = true;
     for (int kb = kb0; kb < kb1; ++kb) {
-      good = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+      good = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag);
       if (!good) break;
       if (threadIdx.x == 0) {
         mbar_arrive_expect_tx(&full_bar[stage], static_cast<uint32_t>(W_MN ? S::W_BYTES : 2 * Rp * 128));
@@ -618,11 +625,11 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     }
     cp_async_commit();
     cp_async_wait<0>();
-    if (!good && threadIdx.x == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
+    if (threadIdx.x == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
     // ---------------- epilogue: row q * 32 + lane of the tile ----------------
     const int q = warp;
     const int r = q * 32 + lane;
-    good = __all_sync(0xffffffffu, good && mbar_wait(tfull_bar, 0, abort_flag)) && kb1 > kb0;
+    good = good && mbar_wait_warp(tfull_bar, 0, abort_flag) && kb1 > kb0;
     tc_fence_after();
     const float s = p.scale != nullptr ? __ldg(p.scale + a) : 1.0f;
     float* out = cluster > 1 ? reinterpret_cast<float*>(smem) + r * (Rp + 4) : p.H + static_cast<int64_t>(r < n ? rows[r] : 0) * p.R;
@@ -664,12 +671,14 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     tc_fence_before();
   } else if (work && lane == 0) {
     // ---------------- MMA issuer ----------------
+    bool good = injected_wait(drain_bar, abort_flag);
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
     const uint32_t idesc = W_MN ? (idesc_f16(LORA_TILE, RB * 64, bf) | IDESC_B_MN) : idesc_f16(LORA_TILE, Rp, bf);
     int stage = 0;
     uint32_t phase = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (!mbar_wait(&full_bar[stage], phase, abort_flag)) break;
+    for (int kb = kb0; good && kb < kb1; ++kb) {
+      good = mbar_wait(&full_bar[stage], phase, abort_flag);
+      if (!good) break;
       fence_proxy_async_smem();   // X was written by cp.async, through the generic proxy
       tc_fence_after();
       const uint32_t as = smem_u32(sA(stage)), ws = smem_u32(sW(stage));
@@ -683,7 +692,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
       umma_commit(&empty_bar[stage]);
       if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
     }
-    umma_commit(tfull_bar);
+    if (good) umma_commit(tfull_bar);
     drain_mma(drain_bar);
   }
   // TMEM goes back before the CTAs of a cluster wait for one another: a peer
@@ -851,7 +860,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
           row_at[i] = row < M ? row_bytes(row, row_size) : -1;
         }
       }
-      good = __all_sync(0xffffffffu, mbar_wait(&yempty_bar[stage], phase ^ 1u, abort_flag));
+      good = mbar_wait_warp(&yempty_bar[stage], phase ^ 1u, abort_flag);
       if (!good) break;
       const int n0 = static_cast<int>(nb) * LORA_EXPAND_BN;
       const uint32_t d = smem_u32(sY(stage)) + r0 * S::Y_ROW + 16 * c;
@@ -912,7 +921,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
           if (u + 1 < u1) a = p.plan.info(static_cast<int>(++t)).x;
         }
       }
-      if (!good) drain_ring(vfull_bar, S::V_STAGES, stage, phase, issued);
+      drain_ring(vfull_bar, S::V_STAGES, stage, phase, issued);
     }
   } else if (warp == 5) {
     if (lane == 0) {
@@ -920,15 +929,14 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
       constexpr uint32_t idesc = idesc_f16(LORA_TILE, LORA_EXPAND_BN, std::is_same<T, __nv_bfloat16>::value) | (V_MN ? IDESC_B_MN : 0u);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, h_phase = 0;
-      bool next = true;
-      for (int64_t u = u0, nb = nb0; u < u1; ++u) {
+      bool next = true, good = injected_wait(drain_bar, abort_flag);
+      for (int64_t u = u0, nb = nb0; good && u < u1; ++u) {
         if (next) {
           if (!mbar_wait(hfull_bar, h_phase, abort_flag)) break;
           h_phase ^= 1u;
         }
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag)) break;
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * LORA_EXPAND_BN);
-        bool good = true;
         for (int b = 0; b < RB; ++b) {   // 64 of R
           good = mbar_wait(&vfull_bar[stage], phase, abort_flag);
           if (!good) break;
@@ -972,7 +980,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
         if (u == u0) {
           griddep_wait();    // H
         } else {             // the MMAs that read the previous tile's parts
-          good = __all_sync(0xffffffffu, mbar_wait(hempty_bar, h_phase, abort_flag));
+          good = mbar_wait_warp(hempty_bar, h_phase, abort_flag);
           if (!good) break;
           h_phase ^= 1u;
         }
@@ -1025,7 +1033,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
         if (lane == 0) mbar_arrive(hfull_bar);
       }
       if (((u - u0) & 1) == group) {
-      good = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[group], acc_phase, abort_flag) && mbar_wait(&yfull_bar[stage], phase, abort_flag));
+      good = mbar_wait_warp(&tfull_bar[group], acc_phase, abort_flag) && mbar_wait_warp(&yfull_bar[stage], phase, abort_flag);
       if (!good) break;
       acc_phase ^= 1u;
       tc_fence_after();
@@ -1306,7 +1314,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       }
       if (u + 1 < u1) look_ahead(t);
       for (int g = 0; g < 2 && c0 + g * 128 < C; ++g) {
-        good = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+        good = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag);
         if (!good) break;
         const uint32_t d = smem_u32(sX(stage)) + off;
         const int col = static_cast<int>(c0) + g * 128 + 8 * c;
@@ -1329,7 +1337,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       constexpr uint32_t idesc = idesc_f16(128, G_COLS, true) | IDESC_A_MN | IDESC_B_MN;
       int stage = 0, gb = 0, acc = 0;
       uint32_t phase = 0, g_phase = 0, acc_phase = 0;
-      bool good = true, open = false;
+      bool good = injected_wait(drain_bar, abort_flag), open = false;
       int t = 0, cg = 0;
       int2 info = make_int2(0, 0);
       if (u0 < u1) {
@@ -1406,7 +1414,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       const int64_t seg0 = static_cast<int64_t>(cg) * un.tiles + p.plan.tile0()[a];
       const int64_t seg1 = static_cast<int64_t>(cg) * un.tiles + p.plan.tile0()[a + 1];
       const int64_t C = (side ? p.cols[1] : p.cols[0]);
-      if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_flag)) break;
+      if (!mbar_wait_warp(&tfull_bar[acc], acc_phase, abort_flag)) break;
       tc_fence_after();
       const bool whole = seg0 >= u0 && seg1 <= u1;
       const float s = side ? __ldg(p.scale + a) : 1.0f;
@@ -1478,7 +1486,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
     for (int64_t u = u0; u < u1; ++u) {
       const uint16_t* G = cg >= un.cg0 ? p.G[1] : p.G[0];
       const int n64 = (n + LORA_WG_ROWS - 1) / LORA_WG_ROWS * LORA_WG_ROWS;
-      if (!__all_sync(0xffffffffu, mbar_wait(&gempty_bar[gb], g_phase ^ 1u, abort_flag))) break;
+      if (!mbar_wait_warp(&gempty_bar[gb], g_phase ^ 1u, abort_flag)) break;
       const uint32_t d = smem_u32(sG(gb)) + off;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
