@@ -466,12 +466,13 @@ QLIN_API qlin_status qlin_get_device_status(int32_t *status, int reset);
 QLIN_API qlin_status qlin_set_wait_timeout_ns(uint64_t ns);
 
 /* Test switch of the failure path (the model-card pages have no counterpart):
- * with on != 0, every later launch of the int8 / FP8 / 16-bit GEMM first waits
- * on a barrier that nothing arrives on, so that its bounded wait runs out
- * after the wait limit (qlin_set_wait_timeout_ns). The kernel then records
- * QLIN_ERR_TIMEOUT in the device status word, stops its other roles, waits
- * (up to max(limit, 1 s)) for its own copies and MMAs in flight, frees its
- * TMEM and returns, leaving Y unwritten; later launches work normally once the
+ * with on != 0, every later launch of a GEMM or of the adapters' tile kernels
+ * first waits on a barrier that nothing arrives on, so that its bounded wait
+ * runs out after the wait limit (qlin_set_wait_timeout_ns). The kernel then
+ * records QLIN_ERR_TIMEOUT in the device status word, stops its other roles,
+ * waits (up to max(limit, 1 s)) for its own copies and MMAs in flight, frees
+ * its TMEM and returns, leaving a GEMM's Y unwritten (an adapter call's outputs
+ * then hold no meaningful values); later launches work normally once the
  * switch is off again. Off by default. Synchronous; call it outside stream
  * capture. */
 QLIN_API qlin_status qlin_debug_inject_wait_timeout(int on);

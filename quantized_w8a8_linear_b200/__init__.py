@@ -671,7 +671,7 @@ def qlin_set_wait_timeout_ns(ns: int) -> None:
 
 
 def qlin_debug_inject_wait_timeout(on: bool) -> None:
-    """Test switch: later GEMM launches wait once on a barrier nothing arrives on (bounded)."""
+    """Test switch: later launches of tcgen05 kernels wait once on a barrier nothing arrives on (bounded)."""
     _check(lib.qlin_debug_inject_wait_timeout(1 if on else 0))
 
 

@@ -21,8 +21,8 @@ namespace qlin {
 __device__ int g_status = 0;
 __device__ unsigned long long g_wait_timeout_ns = 2000000000ull;
 // Test switch of the abort path (off unless qlin_debug_inject_wait_timeout
-// sets it): the MMA warp of k_gemm and of the adapters' tile kernels first
-// waits on a barrier that nothing arrives on, so that its bounded wait runs out.
+// sets it): the MMA warp of a GEMM or an adapters' tile kernel first waits on
+// a barrier that nothing arrives on, so that its bounded wait runs out.
 __device__ int g_inject_wait_timeout = 0;
 
 __device__ __forceinline__ uint64_t globaltimer() {
@@ -122,9 +122,10 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
 
 // Barrier among a group of threads on an mbarrier whose arrival count is the
 // group's thread count, so that the wait is bounded like every other wait.
+// Whole warps call it.
 __device__ __forceinline__ bool epi_bar(uint64_t* bar, uint32_t& phase, volatile int* abort_flag) {
   mbar_arrive(bar);
-  const bool ok = mbar_wait(bar, phase, abort_flag);
+  const bool ok = mbar_wait_warp(bar, phase, abort_flag);
   phase ^= 1u;
   return ok;
 }
@@ -368,6 +369,34 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+
+// Waits (bounded) for the last copies of a producer, in the ring slots before
+// `stage` in issue order as far as they were used: whoever reads them may have
+// given up, and the CTA must not end before they have landed.
+__device__ __forceinline__ void drain_ring(uint64_t* full_bar, int stages, int stage, uint32_t phase, uint32_t issued) {
+  for (int i = 0; i < stages; ++i) {
+    if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
+    if (issued & (1u << stage)) {
+      const uint32_t a = smem_u32(&full_bar[stage]);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(a, phase) && globaltimer() - t0 < drain_limit_ns()) {}
+    }
+  }
+}
+
+// Test of the abort path (qlin_debug_inject_wait_timeout): nothing has
+// committed to the MMA thread's drain barrier yet, so this wait runs out.
+__device__ __forceinline__ bool injected_wait(uint64_t* drain_bar, volatile int* abort_flag) {
+  return g_inject_wait_timeout == 0 || mbar_wait(drain_bar, 0, abort_flag);
+}
+
+// Waits (bounded) for the MMAs this thread issued, before TMEM is freed.
+__device__ __forceinline__ void drain_mma(uint64_t* bar) {
+  umma_commit(bar);
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(a, 0) && globaltimer() - t0 < drain_limit_ns()) {}
 }
 
 // 32 lanes x 32 consecutive 32-bit columns: thread t of the warp gets lane

@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       // ---------------- TMA producer ----------------
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued = 0;   // bit s: stage s has a load in flight that nobody consumed yet
+      uint32_t issued = 0;   // bit s: stage s was used
       bool ok = true;
       SegIter its(sk, num_tiles, p.sk_dp_tiles, num_kb);
       Seg sg;
@@ -756,17 +756,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {
-        // aborted: wait (bounded) for the copies still in flight before the CTA exits
-        for (int i = 0; i < STAGES; ++i) {
-          if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
-          if (issued & (1u << stage)) {
-            const uint32_t a = smem_u32(&full_bar[stage]);
-            const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(a, phase) && globaltimer() - t0 < drain_limit_ns()) {}
-          }
-        }
-      }
+      drain_ring(full_bar, STAGES, stage, phase, issued);
     }
   } else if (warp == GEMM_WARP_MMA) {
     if (lane == 0) {
@@ -778,10 +768,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true;
-      // test of the abort path (qlin_debug_inject_wait_timeout): nothing has
-      // committed to the drain barrier yet, so this bounded wait runs out
-      if (g_inject_wait_timeout != 0) ok = mbar_wait(drain_bar, 0u, abort_flag);
+      bool ok = injected_wait(drain_bar, abort_flag);
       SegIter its(sk, num_tiles, p.sk_dp_tiles, num_kb);
       Seg sg;
       while (ok && its.next(sg)) {
@@ -820,11 +807,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         umma_commit(&tfull_bar[acc]);
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      // every MMA this thread issued has completed before TMEM is released
-      umma_commit(drain_bar);
-      const uint32_t a = smem_u32(drain_bar);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(a, 0) && globaltimer() - t0 < drain_limit_ns()) {}
+      drain_mma(drain_bar);
     }
   }
   } else {
@@ -864,7 +847,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           epi_stage<TOut, EPI, BNG>(p, es, n_base, et, FT && cn > 0 && cnt <= GEMM_OUTL_STAGED ? 0 : cn);
           if (!epi_bar(&epi_mbar[g], bar_phase, abort_flag)) break;
         }
-        if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_flag)) break;
+        if (!mbar_wait_warp(&tfull_bar[acc], acc_phase, abort_flag)) break;
         tc_fence_after();
       } else if constexpr (SK_OK) {
         // A cut tile (stream-K). Every party but one leaves its partial (int32,
@@ -872,7 +855,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         // the owner if all contributors have arrived when its own part is
         // done (then it writes no partial), else the last to arrive. Nobody
         // waits for another CTA.
-        if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_flag)) break;
+        if (!mbar_wait_warp(&tfull_bar[acc], acc_phase, abort_flag)) break;
         tc_fence_after();
         int ob, nc;
         sk_parties(sg.tile, num_kb, num_tiles, p.sk_dp_tiles, ob, nc);

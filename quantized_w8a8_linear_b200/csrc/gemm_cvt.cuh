@@ -254,17 +254,7 @@ __global__ void __launch_bounds__(WO8_THREADS, 1)
           if (++stage == WO8_STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {
-        // aborted: wait (bounded) for the copies still in flight before the CTA exits
-        for (int i = 0; i < WO8_STAGES; ++i) {
-          if (--stage < 0) { stage = WO8_STAGES - 1; phase ^= 1u; }
-          if (issued & (1u << stage)) {
-            const uint32_t a = smem_u32(&full_bar[stage]);
-            const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(a, phase) && globaltimer() - t0 < drain_limit_ns()) {}
-          }
-        }
-      }
+      drain_ring(full_bar, WO8_STAGES, stage, phase, issued);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -272,7 +262,7 @@ __global__ void __launch_bounds__(WO8_THREADS, 1)
       constexpr uint32_t idesc = idesc_f16(WO8_BM, WO8_BN, FMT != 1);   // bf16 (FMT 0, 2) or fp16 operands
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
+      bool ok = injected_wait(drain_bar, abort_flag);
       for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
         if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag)) break;
         tc_fence_after();
@@ -293,11 +283,7 @@ __global__ void __launch_bounds__(WO8_THREADS, 1)
         umma_commit(&tfull_bar[acc]);
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      // every MMA this thread issued has completed before TMEM is released
-      umma_commit(drain_bar);
-      const uint32_t a = smem_u32(drain_bar);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(a, 0) && globaltimer() - t0 < drain_limit_ns()) {}
+      drain_mma(drain_bar);
     }
   } else if (warp >= WO8_WARP_CONV0 && warp < WO8_WARP_CONV0 + WO8_CONV_WARPS) {
     // ---------------- converters: codes * scale -> 16 bits, swizzled ----------------
@@ -326,7 +312,7 @@ __global__ void __launch_bounds__(WO8_THREADS, 1)
         scale_pairs(0, sc);
         for (int kb = 0; kb < num_kb; ++kb) {
           scale_pairs(kb + 1, sn);
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
+          if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
           const uint8_t* raw = sR(stage);
           uint8_t* dst = sB(stage);
 #pragma unroll
@@ -380,7 +366,7 @@ __global__ void __launch_bounds__(WO8_THREADS, 1)
       }
       for (int kb = 0; kb < num_kb; ++kb) {
         if constexpr (FMT == 1) block_scales(kb + 1, sn);
-        if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
         const uint8_t* raw = sR(stage);
         uint8_t* dst = sB(stage);
 #pragma unroll
@@ -425,7 +411,7 @@ __global__ void __launch_bounds__(WO8_THREADS, 1)
         bt[j] = (p.bias != nullptr && n < N) ? to_f<TOut>(__ldg(p.bias + n)) : 0.0f;
       }
       if (!epi_bar(epi_mbar, bar_phase, abort_flag)) break;
-      if (!mbar_wait(&tfull_bar[acc], acc_phase, abort_flag)) break;
+      if (!mbar_wait_warp(&tfull_bar[acc], acc_phase, abort_flag)) break;
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * WO8_BN);
       uint32_t r[32];

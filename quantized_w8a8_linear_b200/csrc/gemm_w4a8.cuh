@@ -209,16 +209,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
           if (++stage == W4_STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {
-        for (int i = 0; i < W4_STAGES; ++i) {
-          if (--stage < 0) { stage = W4_STAGES - 1; phase ^= 1u; }
-          if (issued & (1u << stage)) {
-            const uint32_t a = smem_u32(&full_bar[stage]);
-            const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(a, phase) && globaltimer() - t0 < drain_limit_ns()) {}
-          }
-        }
-      }
+      drain_ring(full_bar, W4_STAGES, stage, phase, issued);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -228,7 +219,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
       uint32_t phase = 0, uphase = 0;
       int buf = 0;
       uint32_t buf_phase = 0;
-      bool ok = true;
+      bool ok = injected_wait(drain_bar, abort_flag);
       for (int tile = blockIdx.x; ok && tile < num_tiles; tile += gridDim.x) {
         for (int g = 0; g < G; ++g) {
           // the u-th use of an accumulator waits for its u-th release (the first is at start-up)
@@ -250,10 +241,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
           if (++buf == W4_ACC) { buf = 0; buf_phase ^= 1u; }
         }
       }
-      umma_commit(drain_bar);
-      const uint32_t a = smem_u32(drain_bar);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(a, 0) && globaltimer() - t0 < drain_limit_ns()) {}
+      drain_mma(drain_bar);
     }
   } else {
     // ---------------- converters: packed int4 -> swizzled int8 ----------------
@@ -263,8 +251,8 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
       bool ok = true;
       for (int g = 0; g < G; ++g) {
-        if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
-        if (!mbar_wait(&uempty_bar[u], uphase ^ 1u, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_warp(&uempty_bar[u], uphase ^ 1u, abort_flag)) { ok = false; break; }
         const uint4* src = reinterpret_cast<const uint4*>(sBp(stage));
         uint8_t* dst = sBu(u);
 #pragma unroll 2
@@ -336,7 +324,7 @@ __global__ void __launch_bounds__(W4_THREADS, 1)
       };
       // wait until the MMA has finished accumulator `buf`, then start reading chunk 0 of it
       auto fetch = [&](uint32_t (&r)[8]) -> bool {
-        if (!mbar_wait(&gfull_bar[buf], buf_phase, abort_flag)) return false;
+        if (!mbar_wait_warp(&gfull_bar[buf], buf_phase, abort_flag)) return false;
         tc_fence_after();
         __syncwarp();
         tmem_ld8(taddr(buf, 0), r);

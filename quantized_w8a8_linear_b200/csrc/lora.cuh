@@ -273,34 +273,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
-// Waits (bounded) for the last copies of a producer, in the ring slots before
-// `stage` in issue order as far as they were used: whoever reads them may have
-// given up, and the CTA must not end before they have landed.
-__device__ __forceinline__ void drain_ring(uint64_t* full_bar, int stages, int stage, uint32_t phase, uint32_t issued) {
-  for (int i = 0; i < stages; ++i) {
-    if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
-    if (issued & (1u << stage)) {
-      const uint32_t a = smem_u32(&full_bar[stage]);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(a, phase) && globaltimer() - t0 < drain_limit_ns()) {}
-    }
-  }
-}
-
-// Test of the abort path (qlin_debug_inject_wait_timeout): nothing has
-// committed to the MMA thread's drain barrier yet, so this wait runs out.
-__device__ __forceinline__ bool injected_wait(uint64_t* drain_bar, volatile int* abort_flag) {
-  return g_inject_wait_timeout == 0 || mbar_wait(drain_bar, 0, abort_flag);
-}
-
-// Waits (bounded) for the MMAs this thread issued, before TMEM is freed.
-__device__ __forceinline__ void drain_mma(uint64_t* bar) {
-  umma_commit(bar);
-  const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(a, 0) && globaltimer() - t0 < drain_limit_ns()) {}
-}
-
 // 8 fp32 values -> three 16-byte chunks of 16-bit values whose sum is the
 // value. Where the first is not finite the others are 0, so an infinite or NaN
 // value stays what it is.
