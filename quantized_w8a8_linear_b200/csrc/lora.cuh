@@ -1145,7 +1145,12 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
 // tile fastest and are cut into one equal range per CTA. The tile of X is the
 // A operand and the parts of G the B operand, both MN-major as they lie in
 // memory (one 128-byte row per step of the contraction), so nothing is
-// transposed. Sums stay in TMEM over the tiles of an adapter. An adapter whose
+// transposed. Sums stay in TMEM over the tiles of an adapter: an MMA cuts its
+// accumulator off instead of rounding it, so every LORA_WG_CHAIN tiles the
+// epilogue adds it, rounded, to sums of its own beside it (one chain over 8192
+// positive rows came out 5e-5 too small, chains of 1024 rows 6e-6). The
+// accumulators of a unit's two MMAs are handed back one by one, and the copies
+// run on meanwhile, so it costs no time. An adapter whose
 // tiles are cut between CTAs leaves fp32 partial sums, slot 0 for a CTA's
 // first segment if it began before, slot 1 for the last one, and
 // k_lora_wgrad_join adds them in CTA order. 8191 rows, 4096 and 12288 columns,
@@ -1156,6 +1161,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
 constexpr int LORA_WG_THREADS = 416;   // warps 0-3 copy X, warp 4 MMA, warps 5-8 epilogue, warps 9-12 copy G
 constexpr int LORA_WG_COLS = 256;      // columns of a unit: two MMAs of M = 128
 constexpr int LORA_WG_ROWS = 64;       // rows of a block of MMAs: a tile has one or two
+constexpr int LORA_WG_CHAIN = 8;       // tiles of a chain of MMAs (4 above rank 64)
 
 struct LoraWgradParams {
   LoraPlan plan;
@@ -1205,7 +1211,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   uint64_t* empty_bar = full_bar + S::STAGES;
   uint64_t* gfull_bar = empty_bar + S::STAGES;   // [2]
   uint64_t* gempty_bar = gfull_bar + 2;          // [2]
-  uint64_t* tfull_bar = gempty_bar + 2;          // [2]
+  uint64_t* tfull_bar = gempty_bar + 2;          // [2], of the accumulators of a unit's two MMAs
   uint64_t* tempty_bar = tfull_bar + 2;          // [2]
   uint64_t* drain_bar = tempty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -1215,9 +1221,10 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   // took the MMA thread 65 us for 8191 rows against 50 us of HBM time
   constexpr bool BOTH = RB == 1;
   constexpr uint32_t G_COLS = BOTH ? 128 : RB * 64;   // accumulator columns of 128 columns of X
-  constexpr uint32_t ACC_COLS = 2 * G_COLS;
-  constexpr uint32_t TCOLS = 2 * ACC_COLS;
-  static_assert(TCOLS <= 512, "TMEM");
+  constexpr uint32_t SUMS = 2 * G_COLS, SUM_COLS = RB * 64;   // the rounded sums behind the two accumulators
+  constexpr uint32_t TCOLS = 512;
+  static_assert(SUMS + 2 * SUM_COLS <= TCOLS, "TMEM");
+  constexpr int CHAIN = LORA_WG_CHAIN / RB;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1307,9 +1314,9 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16(128, G_COLS, true) | IDESC_A_MN | IDESC_B_MN;
-      int stage = 0, gb = 0, acc = 0;
-      uint32_t phase = 0, g_phase = 0, acc_phase = 0;
-      bool good = injected_wait(drain_bar, abort_flag), open = false;
+      int stage = 0, gb = 0, chain = 0;   // tiles in the accumulators
+      uint32_t phase = 0, g_phase = 0, acc_phase = 0;   // a bit for each accumulator
+      bool good = injected_wait(drain_bar, abort_flag);
       int t = 0, cg = 0;
       int2 info = make_int2(0, 0);
       if (u0 < u1) {
@@ -1327,11 +1334,16 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
           ++cg;
         }
         if (u + 1 < u1) info = p.plan.info(t);   // looked up a unit ahead
-        if (!open && !mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, abort_flag)) break;
+        const bool more_tiles = chain > 0;
+        const bool close = ++chain == CHAIN || u + 1 == u1 || last || info.x != here.x;
         if (!mbar_wait(&gfull_bar[gb], g_phase, abort_flag)) break;
         const uint32_t gs = smem_u32(sG(gb));
         for (int g = 0; good && g < 2 && c0 + g * 128 < (side ? p.cols[1] : p.cols[0]); ++g) {
-          const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g) * G_COLS;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(g) * G_COLS;
+          if (!more_tiles) {
+            if (!mbar_wait(&tempty_bar[g], (acc_phase >> g & 1u) ^ 1u, abort_flag)) { good = false; break; }
+            acc_phase ^= 1u << g;
+          }
           if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { good = false; break; }
           fence_proxy_async_smem();   // X and G were written by cp.async, through the generic proxy
           tc_fence_after();
@@ -1341,22 +1353,19 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
             if (LORA_WG_ROWS * h >= here.y) break;
             const uint64_t adesc = sdesc_mn128(smem_u32(sX(stage)) + h * (LORA_WG_ROWS * 128), LORA_TILE * 128);
             const uint64_t bdesc = sdesc_mn128(gs + h * (LORA_WG_ROWS * 128), BOTH ? S::G_BYTES : LORA_TILE * 128);
-            const uint32_t more = open || h > 0 ? 1u : 0u;
+            const uint32_t more = more_tiles || h > 0 ? 1u : 0u;
 #pragma unroll
             for (int k = 0; k < (BOTH ? 1 : 2) * KS; ++k)   // the parts of G: side by side, or one after the other
               umma<2>(d, adesc + 128u * (k % KS), bdesc + 128u * (k % KS) + (k / KS) * (S::G_BYTES >> 4), idesc, k == 0 ? more : 1u);
           }
           umma_commit(&empty_bar[stage]);
           if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+          if (close) umma_commit(&tfull_bar[g]);
         }
         if (!good) break;
         umma_commit(&gempty_bar[gb]);
         if (++gb == 2) { gb = 0; g_phase ^= 1u; }
-        open = u + 1 < u1 && !last && info.x == here.x;
-        if (!open) {
-          umma_commit(&tfull_bar[acc]);
-          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-        }
+        if (close) chain = 0;
       }
       drain_mma(drain_bar);
     }
@@ -1376,61 +1385,73 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       }
     }
     const int q = warp & 3;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int64_t u = u0; u < u1;) {
+    const uint32_t tmem = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t acc_phase = 0;   // a bit for each accumulator
+    bool good = true;
+    for (int64_t u = u0; good && u < u1;) {   // one segment: the tiles of an adapter in this CTA's range, under one group of columns
       const int cg = static_cast<int>(u / un.tiles), t = static_cast<int>(u % un.tiles);
       const int side = cg >= un.cg0;
       const int64_t c0 = static_cast<int64_t>(cg - (side ? un.cg0 : 0)) * LORA_WG_COLS;
       const int a = p.plan.info(t).x;
       const int64_t seg0 = static_cast<int64_t>(cg) * un.tiles + p.plan.tile0()[a];
       const int64_t seg1 = static_cast<int64_t>(cg) * un.tiles + p.plan.tile0()[a + 1];
-      const int64_t C = (side ? p.cols[1] : p.cols[0]);
-      if (!mbar_wait_warp(&tfull_bar[acc], acc_phase, abort_flag)) break;
-      tc_fence_after();
+      const int64_t C = (side ? p.cols[1] : p.cols[0]), end = seg1 < u1 ? seg1 : u1;
       const bool whole = seg0 >= u0 && seg1 <= u1;
       const float s = side ? __ldg(p.scale + a) : 1.0f;
       float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (seg0 >= u0 ? 1 : 0)) * p.R * LORA_WG_COLS;
-      for (int g = 0; g < 2 && c0 + g * 128 < C; ++g) {
-        const int64_t col = c0 + g * 128 + q * 32 + lane;
-        const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * ACC_COLS + static_cast<uint32_t>(g) * G_COLS;
-        for (int c = 0; c < p.R; c += 16) {
-          uint32_t v[16];
-          __syncwarp();
-          tmem_ld16(at + static_cast<uint32_t>(c), v);
-          tmem_wait16(v);
-          if constexpr (BOTH) {
-            uint32_t lo[16];
-            tmem_ld16(at + static_cast<uint32_t>(64 + c), lo);
-            tmem_wait16(lo);
+      for (int64_t v0 = u; good && v0 < end; v0 += CHAIN) {
+        const bool first = v0 == u, last = v0 + CHAIN >= end;
+        for (int g = 0; g < 2 && c0 + g * 128 < C; ++g) {
+          good = mbar_wait_warp(&tfull_bar[g], acc_phase >> g & 1u, abort_flag);
+          if (!good) break;
+          acc_phase ^= 1u << g;
+          tc_fence_after();
+          const int64_t col = c0 + g * 128 + q * 32 + lane;
+          const uint32_t at = tmem + static_cast<uint32_t>(g) * G_COLS, sums = tmem + SUMS + static_cast<uint32_t>(g) * SUM_COLS;
+          for (int c = 0; c < p.R; c += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld16(at + static_cast<uint32_t>(c), v);
+            tmem_wait16(v);
+            auto add = [&](uint32_t from) {
+              uint32_t w[16];
+              tmem_ld16(from + static_cast<uint32_t>(c), w);
+              tmem_wait16(w);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(lo[i]));
-          }
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+            };
+            if constexpr (BOTH) add(at + 64);
+            if (!first) add(sums);
+            if (!last) {
+              tmem_st16(sums + static_cast<uint32_t>(c), v);
+              continue;
+            }
 #pragma unroll
-          for (int h = 0; h < 16; h += 8) {
-            if (c + h < p.R && col < C) {
-              if (!whole) {
+            for (int h = 0; h < 16; h += 8) {
+              if (c + h < p.R && col < C) {
+                if (!whole) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) part[(c + h + i) * LORA_WG_COLS + g * 128 + q * 32 + lane] = __uint_as_float(v[h + i]);
-              } else if (side == 0) {
+                  for (int i = 0; i < 8; ++i) part[(c + h + i) * LORA_WG_COLS + g * 128 + q * 32 + lane] = __uint_as_float(v[h + i]);
+                } else if (side == 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p.out[0][(static_cast<int64_t>(a) * p.R + c + h + i) * C + col] = from_f<T>(__uint_as_float(v[h + i]));
-              } else {
-                float f[8];
+                  for (int i = 0; i < 8; ++i) p.out[0][(static_cast<int64_t>(a) * p.R + c + h + i) * C + col] = from_f<T>(__uint_as_float(v[h + i]));
+                } else {
+                  float f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[h + i]) * s;
-                *reinterpret_cast<uint4*>(p.out[1] + (static_cast<int64_t>(a) * C + col) * p.R + c + h) =
-                    make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+                  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[h + i]) * s;
+                  *reinterpret_cast<uint4*>(p.out[1] + (static_cast<int64_t>(a) * C + col) * p.R + c + h) =
+                      make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+                }
               }
             }
           }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty_bar[g]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty_bar[acc]);
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-      u = seg1 < u1 ? seg1 : u1;
+      u = end;
     }
   } else {
     // ---------------- copies of G's parts, one tile a unit: chunk c of rows r0, r0 + step, ... of both parts ----------------

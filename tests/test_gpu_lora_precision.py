@@ -103,3 +103,21 @@ def test_dx_sees_all_bits_of_dh(q, R):
     base = -update.to(dtype)
     dX, _, _ = q.qlin_lora_backward(dY, X, A, B, scale, q.qlin_lora_plan(idx, L), torch.zeros((M, R), device="cuda"), dX=base.clone())
     _check_difference(dX, base, update, dtype)
+
+
+def test_gradient_is_summed_in_short_chains(q):
+    # 8192 rows of one adapter under columns enough that a CTA takes all of a column's tiles: 512 MMAs in line, in chains
+    # of 64, for each element of dB. bf16's steps are 2^-8 to 2^-7 of a value, and the elements lie anywhere between them
+    # (a factor for each column), so of sums that are too small by e on average at most 2^8 e are rounded the other way.
+    # What is cut off is half of the most on average: two steps an MMA. H in 8 bits, so that it is its own first part.
+    M, K, N, R, dtype = 8192, 26112, 12288, 8, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dY = ((0.5 + torch.rand((M, N), generator=g, device="cuda")) * 2.0 ** torch.rand(N, generator=g, device="cuda")).to(dtype)
+    X = torch.ones((M, K), dtype=dtype, device="cuda")
+    A, B = torch.ones((1, R, K), dtype=dtype, device="cuda"), torch.ones((1, N, R), dtype=dtype, device="cuda")
+    H = _positive(g, (M, R), dtype).float()
+    plan = q.qlin_lora_plan(torch.zeros(M, dtype=torch.int32, device="cuda"), 1)
+    _, _, dB = q.qlin_lora_backward(dY, X, A, B, torch.ones(1, device="cuda"), plan, H)
+    want = torch.cat([dY[:, n:n + 1024].double().T @ H.double() for n in range(0, N, 1024)]).to(dtype)
+    e = 2 * (64 + 1) / 2 * 2.0 ** -23 + 8 * 2.0 ** -25
+    assert (dB[0] != want).float().mean().item() <= 2.0 ** 8 * e
