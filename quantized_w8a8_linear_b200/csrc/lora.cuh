@@ -22,13 +22,14 @@
 // A few rows (a decode step) go through k_lora_rows instead, one launch for
 // both products of up to eight rows of one adapter.
 //
-// H enters the second product as three 16-bit parts, T(h), T of what that
+// H and dH enter the other products as three 16-bit parts, T(h), T of what that
 // leaves and T of what both leave, three MMAs on one staged operand: fp32's 24
 // bits, so that a row comes out the same as where H stays fp32 (k_lora_rows).
 // With two parts, 16 bits in bf16, 2^-17 of the update showed in Y where it
 // cancels, and more of Y's elements than an fp32 product has rounded the other
-// way; the third one costs 1 to 5% (16640 x 4096 -> 12288, rank 64: 198 us in
-// all, 190 with two). The smallest go first, while the accumulator is small. fp16
+// way; the third one costs the forward pass 1 to 5% (16640 x 4096 -> 12288,
+// rank 64: 198 us in all, 190 with two) and the backward pass 2 to 6%, 17% above
+// rank 64. The smallest go first, while the accumulator is small. fp16
 // parts are taken of h 2^14 / 2^e with 2^e the largest power of two in the row
 // (exact): nothing overflows, all 24 bits of what is above 2^-15 of the row's
 // largest are kept, and of the rest all above 2^-39 of it.
@@ -292,14 +293,14 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4 (&part)[3]) {
     part[j] = make_uint4(h[j][0] | (h[j][1] << 16), h[j][2] | (h[j][3] << 16), h[j][4] | (h[j][5] << 16), h[j][6] | (h[j][7] << 16));
 }
 
-// The same for 4 values, written to row[0] and row[R] of a split row [2][R].
+// The same for 4 values, written to row[0], row[R] and row[2 R] of a split row [3][R].
 template <typename T>
 __device__ __forceinline__ void store_split4(uint16_t* row, int R, const float4& v) {
   const float f[8] = {v.x, v.y, v.z, v.w};
   uint4 part[3];
   split8<T>(f, part);
-  *reinterpret_cast<uint2*>(row) = make_uint2(part[0].x, part[0].y);
-  *reinterpret_cast<uint2*>(row + R) = make_uint2(part[1].x, part[1].y);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) *reinterpret_cast<uint2*>(row + j * R) = make_uint2(part[j].x, part[j].y);
 }
 
 // ---------------------------------------------------------------------------
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(LORA_ROWS_THREADS, 2) k_lora_rows(const LoraRo
 // of all of them in rank order (distributed shared memory; no workspace and
 // no second kernel). c is chosen so that few tiles still fill the SMs.
 // In the backward pass (W_MN 1) it also leaves dH and the forward's H as split
-// rows [2][R] for k_lora_wgrad, whose every CTA reads all of them.
+// rows [3][R] for k_lora_wgrad, whose every CTA reads all of them.
 // ---------------------------------------------------------------------------
 constexpr int LORA_SHRINK_THREADS = 160;   // warps 0-3 copies, then the epilogue; warp 4 MMA
 constexpr int LORA_SHRINK_BK = 128;        // contraction of a stage: 256 bytes of a row
@@ -479,9 +480,9 @@ struct LoraShrinkParams {
   const float* scale;   // [L], or nullptr: 1
   float* H;             // [M,R]
   // W_MN 1:
-  uint16_t* Hs;         // [M,2,R] the parts of H
+  uint16_t* Hs;         // [M,3,R] the parts of H
   const float* G;       // [M,R] another matrix to split
-  uint16_t* Gs;         // [M,2,R]
+  uint16_t* Gs;         // [M,3,R]
 };
 
 // RB: ceil(R / 64). DEEP: one CTA an SM with four stages, for tiles enough to
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
               if (!good) f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               if (cluster == 1) {
                 f = make_float4(f.x * s, f.y * s, f.z * s, f.w * s);
-                if constexpr (W_MN) store_split4<T>(p.Hs + static_cast<int64_t>(rows[r]) * 2 * p.R + c0 + i, p.R, f);
+                if constexpr (W_MN) store_split4<T>(p.Hs + static_cast<int64_t>(rows[r]) * 3 * p.R + c0 + i, p.R, f);
               }
               *reinterpret_cast<float4*>(out + c0 + i) = f;
             }
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
         sum = make_float4(sum.x * s, sum.y * s, sum.z * s, sum.w * s);
         const int64_t row = p.plan.rows(tile)[r];
         *reinterpret_cast<float4*>(p.H + row * p.R + c) = sum;
-        if constexpr (W_MN) store_split4<T>(p.Hs + row * 2 * p.R + c, p.R, sum);
+        if constexpr (W_MN) store_split4<T>(p.Hs + row * 3 * p.R + c, p.R, sum);
       }
     }
     cluster_sync();   // no CTA leaves while another reads its partial tile
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     for (int e = threadIdx.x; e < mine * r4; e += LORA_SHRINK_THREADS) {
       const int64_t row = p.plan.rows(tile)[rank + e / r4 * cluster];
       const int c = e % r4 * 4;
-      store_split4<T>(p.Gs + row * 2 * p.R + c, p.R, *reinterpret_cast<const float4*>(p.G + row * p.R + c));
+      store_split4<T>(p.Gs + row * 3 * p.R + c, p.R, *reinterpret_cast<const float4*>(p.G + row * p.R + c));
     }
   }
 }
@@ -1168,7 +1169,7 @@ struct LoraWgradParams {
   int R, ctas;
   int64_t cols[2];       // K, N
   const uint16_t* X[2];  // X [M,K], dY [M,N]
-  const uint16_t* G[2];  // dH, H as split rows [M,2,R]
+  const uint16_t* G[2];  // dH, H as split rows [M,3,R]
   const float* scale;    // [L]
   uint16_t* out[2];      // dA [L,R,K], dB [L,N,R]
   float* part;           // [ctas][2][R][256] fp32
@@ -1191,11 +1192,13 @@ struct LoraWgradUnits {
 
 template <int RB>
 struct LoraWgradSmem {
-  static constexpr int STAGES = RB == 1 ? 5 : 3;
+  static constexpr int STAGES = 4;
   static constexpr int X_BYTES = 2 * LORA_TILE * 128;            // 128 columns of the tile: two 64-column halves
-  static constexpr int G_BYTES = RB * LORA_TILE * 128;           // one part
-  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 9) + 16;
-  static constexpr int TOTAL = 1024 + STAGES * X_BYTES + 4 * G_BYTES + BAR_BYTES;
+  static constexpr int G_BUFS = 2;
+  static constexpr int G_ROWS = LORA_TILE / RB;                  // rows of a buffer of G: a tile, above rank 64 half of one
+  static constexpr int G_BYTES = RB * G_ROWS * 128;              // one part
+  static constexpr int BAR_BYTES = 8 * (2 * STAGES + 2 * G_BUFS + 5) + 16;
+  static constexpr int TOTAL = 1024 + STAGES * X_BYTES + G_BUFS * 3 * G_BYTES + BAR_BYTES;
   static_assert(TOTAL <= 227 * 1024, "k_lora_wgrad shared memory");
 };
 
@@ -1206,21 +1209,23 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto sX = [&](int s) { return smem + s * S::X_BYTES; };
-  auto sG = [&](int b) { return smem + S::STAGES * S::X_BYTES + b * 2 * S::G_BYTES; };   // [hi, lo]
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::X_BYTES + 4 * S::G_BYTES);
+  auto sG = [&](int b) { return smem + S::STAGES * S::X_BYTES + b * 3 * S::G_BYTES; };   // [3 parts]
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + S::STAGES * S::X_BYTES + S::G_BUFS * 3 * S::G_BYTES);
   uint64_t* empty_bar = full_bar + S::STAGES;
-  uint64_t* gfull_bar = empty_bar + S::STAGES;   // [2]
-  uint64_t* gempty_bar = gfull_bar + 2;          // [2]
-  uint64_t* tfull_bar = gempty_bar + 2;          // [2], of the accumulators of a unit's two MMAs
+  uint64_t* gfull_bar = empty_bar + S::STAGES;
+  uint64_t* gempty_bar = gfull_bar + S::G_BUFS;
+  uint64_t* tfull_bar = gempty_bar + S::G_BUFS;           // [2], of the accumulators of a unit's two MMAs
   uint64_t* tempty_bar = tfull_bar + 2;          // [2]
   uint64_t* drain_bar = tempty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // R <= 64: one MMA multiplies both parts (N = 128: hi | lo, added by the
-  // epilogue), so that X's tile is read from shared memory once; two of N = 64
-  // took the MMA thread 65 us for 8191 rows against 50 us of HBM time
-  constexpr bool BOTH = RB == 1;
-  constexpr uint32_t G_COLS = BOTH ? 128 : RB * 64;   // accumulator columns of 128 columns of X
+  // R <= 64: one MMA multiplies all parts (N = 192: side by side, added by the
+  // epilogue), so that X's tile is read from shared memory once; above, one MMA
+  // a part, into the same accumulator. A buffer of G then holds 64 rows (four
+  // buffers of 32 rows: 8192 x 4096 -> 12288 at rank 72, the whole backward
+  // pass, 235 us; two of 64 rows 210).
+  constexpr bool ALL = RB == 1;
+  constexpr uint32_t G_COLS = ALL ? 192 : 128;   // accumulator columns of 128 columns of X
   constexpr uint32_t SUMS = 2 * G_COLS, SUM_COLS = RB * 64;   // the rounded sums behind the two accumulators
   constexpr uint32_t TCOLS = 512;
   static_assert(SUMS + 2 * SUM_COLS <= TCOLS, "TMEM");
@@ -1232,9 +1237,11 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       mbar_init(&full_bar[s], 128);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < S::G_BUFS; ++b) {
       mbar_init(&gfull_bar[b], 128);
       mbar_init(&gempty_bar[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], 4);
     }
@@ -1313,7 +1320,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   } else if (warp == 4) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idesc = idesc_f16(128, G_COLS, true) | IDESC_A_MN | IDESC_B_MN;
+      const uint32_t idesc = idesc_f16(128, ALL ? static_cast<int>(G_COLS) : (p.R + 15) / 16 * 16, true) | IDESC_A_MN | IDESC_B_MN;
       int stage = 0, gb = 0, chain = 0;   // tiles in the accumulators
       uint32_t phase = 0, g_phase = 0, acc_phase = 0;   // a bit for each accumulator
       bool good = injected_wait(drain_bar, abort_flag);
@@ -1336,35 +1343,49 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
         if (u + 1 < u1) info = p.plan.info(t);   // looked up a unit ahead
         const bool more_tiles = chain > 0;
         const bool close = ++chain == CHAIN || u + 1 == u1 || last || info.x != here.x;
-        if (!mbar_wait(&gfull_bar[gb], g_phase, abort_flag)) break;
-        const uint32_t gs = smem_u32(sG(gb));
-        for (int g = 0; good && g < 2 && c0 + g * 128 < (side ? p.cols[1] : p.cols[0]); ++g) {
-          const uint32_t d = tmem_base + static_cast<uint32_t>(g) * G_COLS;
-          if (!more_tiles) {
-            if (!mbar_wait(&tempty_bar[g], (acc_phase >> g & 1u) ^ 1u, abort_flag)) { good = false; break; }
-            acc_phase ^= 1u << g;
-          }
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { good = false; break; }
-          fence_proxy_async_smem();   // X and G were written by cp.async, through the generic proxy
-          tc_fence_after();
-          constexpr int KS = LORA_WG_ROWS / 16;
+        const int cols = c0 + 128 < (side ? p.cols[1] : p.cols[0]) ? 2 : 1;   // MMAs of 128 columns
+#pragma unroll 1
+        for (int b = 0; b < LORA_TILE / S::G_ROWS; ++b) {   // buffers of G
+          if (S::G_ROWS * b >= here.y) break;
+          good = mbar_wait(&gfull_bar[gb], g_phase, abort_flag);
+          for (int g = 0; good && g < cols; ++g) {
+            const int at = stage + g < S::STAGES ? stage + g : stage + g - S::STAGES;
+            const uint32_t d = tmem_base + static_cast<uint32_t>(g) * G_COLS;
+            if (b == 0) {
+              if (!more_tiles) {
+                good = mbar_wait(&tempty_bar[g], (acc_phase >> g & 1u) ^ 1u, abort_flag);
+                acc_phase ^= 1u << g;
+              }
+              good = good && mbar_wait(&full_bar[at], stage + g < S::STAGES ? phase : phase ^ 1u, abort_flag);
+              if (!good) break;
+            }
+            fence_proxy_async_smem();   // X and G were written by cp.async, through the generic proxy
+            tc_fence_after();
+            constexpr int KS = LORA_WG_ROWS / 16;
 #pragma unroll
-          for (int h = 0; h < LORA_TILE / LORA_WG_ROWS; ++h) {
-            if (LORA_WG_ROWS * h >= here.y) break;
-            const uint64_t adesc = sdesc_mn128(smem_u32(sX(stage)) + h * (LORA_WG_ROWS * 128), LORA_TILE * 128);
-            const uint64_t bdesc = sdesc_mn128(gs + h * (LORA_WG_ROWS * 128), BOTH ? S::G_BYTES : LORA_TILE * 128);
-            const uint32_t more = more_tiles || h > 0 ? 1u : 0u;
+            for (int h = 0; h < S::G_ROWS / LORA_WG_ROWS; ++h) {
+              const int row = S::G_ROWS * b + LORA_WG_ROWS * h;
+              if (row >= here.y) break;
+              const uint64_t adesc = sdesc_mn128(smem_u32(sX(at)) + row * 128, LORA_TILE * 128);
+              const uint64_t bdesc = sdesc_mn128(smem_u32(sG(gb)) + h * (LORA_WG_ROWS * 128), ALL ? S::G_BYTES : S::G_ROWS * 128);
+              const uint32_t more = more_tiles || row > 0 ? 1u : 0u;
 #pragma unroll
-            for (int k = 0; k < (BOTH ? 1 : 2) * KS; ++k)   // the parts of G: side by side, or one after the other
-              umma<2>(d, adesc + 128u * (k % KS), bdesc + 128u * (k % KS) + (k / KS) * (S::G_BYTES >> 4), idesc, k == 0 ? more : 1u);
+              for (int k = 0; k < (ALL ? 1 : 3) * KS; ++k) {   // the parts of G: side by side, or the smallest first
+                const int part = ALL ? 0 : 2 - k / KS;
+                umma<2>(d, adesc + 128u * (k % KS), bdesc + 128u * (k % KS) + part * (S::G_BYTES >> 4), idesc, k == 0 ? more : 1u);
+              }
+            }
+            if (S::G_ROWS * (b + 1) >= here.y) {   // the tile's last rows
+              umma_commit(&empty_bar[at]);
+              if (close) umma_commit(&tfull_bar[g]);
+            }
           }
-          umma_commit(&empty_bar[stage]);
-          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
-          if (close) umma_commit(&tfull_bar[g]);
+          if (!good) break;
+          umma_commit(&gempty_bar[gb]);
+          if (++gb == S::G_BUFS) { gb = 0; g_phase ^= 1u; }
         }
-        if (!good) break;
-        umma_commit(&gempty_bar[gb]);
-        if (++gb == 2) { gb = 0; g_phase ^= 1u; }
+        stage += cols;
+        if (stage >= S::STAGES) { stage -= S::STAGES; phase ^= 1u; }
         if (close) chain = 0;
       }
       drain_mma(drain_bar);
@@ -1420,7 +1441,10 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
             };
-            if constexpr (BOTH) add(at + 64);
+            if constexpr (ALL) {
+              add(at + 64);
+              add(at + 128);
+            }
             if (!first) add(sums);
             if (!last) {
               tmem_st16(sums + static_cast<uint32_t>(c), v);
@@ -1454,12 +1478,12 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
       u = end;
     }
   } else {
-    // ---------------- copies of G's parts, one tile a unit: chunk c of rows r0, r0 + step, ... of both parts ----------------
+    // ---------------- copies of G's parts, one tile a unit: chunk c of rows r0, r0 + step, ... of all parts ----------------
     constexpr int CH = RB * 8;                 // 16-byte chunks of a row of a part
     constexpr int STEP = 128 / CH, PER = LORA_TILE / STEP;
     const int ct = threadIdx.x - 32 * 9;
     const int c = ct % CH, r0 = ct / CH;
-    const uint32_t off = static_cast<uint32_t>((c >> 3) * (LORA_TILE * 128) + r0 * 128);
+    const uint32_t off = static_cast<uint32_t>((c >> 3) * (S::G_ROWS * 128) + r0 * 128);
     int gb = 0, t = 0, cg = 0, n = 0;
     uint32_t g_phase = 0;
     int row[PER];   // the thread's rows of a unit, looked up a unit ahead; -1 past the count
@@ -1479,26 +1503,33 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
     for (int64_t u = u0; u < u1; ++u) {
       const uint16_t* G = cg >= un.cg0 ? p.G[1] : p.G[0];
       const int n64 = (n + LORA_WG_ROWS - 1) / LORA_WG_ROWS * LORA_WG_ROWS;
-      if (!mbar_wait_warp(&gempty_bar[gb], g_phase ^ 1u, abort_flag)) break;
-      const uint32_t d = smem_u32(sG(gb)) + off;
+      bool good = true;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int r = r0 + STEP * i;
-        if (r < n64) {
-          const bool on = row[i] >= 0 && 8 * c < p.R;
-          const uint16_t* src = G + row_bytes(row[i], 2 * p.R) + 8 * c;   // in elements
-          const uint32_t at = d + 128u * STEP * i + (((c & 7) ^ (r & 7)) << 4);
-          cp_async16_or_zero(at, src, on);
-          cp_async16_or_zero(at + S::G_BYTES, src + p.R, on);
+      for (int b = 0; b < LORA_TILE / S::G_ROWS; ++b) {
+        if (S::G_ROWS * b >= n) break;
+        good = mbar_wait_warp(&gempty_bar[gb], g_phase ^ 1u, abort_flag);
+        if (!good) break;
+        const uint32_t d = smem_u32(sG(gb)) + off;
+#pragma unroll
+        for (int i = 0; i < S::G_ROWS / STEP; ++i) {
+          const int r = r0 + STEP * i, m = row[b * (S::G_ROWS / STEP) + i];   // row of the buffer, and of the batch
+          if (S::G_ROWS * b + r < n64) {
+            const bool on = m >= 0 && 8 * c < p.R;
+            const uint16_t* src = G + row_bytes(m, 3 * p.R) + 8 * c;   // in elements
+            const uint32_t at = d + 128u * STEP * i + (((c & 7) ^ (r & 7)) << 4);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) cp_async16_or_zero(at + j * S::G_BYTES, src + j * p.R, on);
+          }
         }
+        cp_async_arrive(&gfull_bar[gb]);
+        if (++gb == S::G_BUFS) { gb = 0; g_phase ^= 1u; }
       }
-      cp_async_arrive(&gfull_bar[gb]);
+      if (!good) break;
       if (++t == un.tiles) {
         t = 0;
         ++cg;
       }
       if (u + 1 < u1) look_up();
-      if (++gb == 2) { gb = 0; g_phase ^= 1u; }
     }
     cp_async_commit();
     cp_async_wait<0>();

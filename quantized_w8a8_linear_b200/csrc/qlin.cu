@@ -1792,7 +1792,7 @@ size_t qlin_lora_forward_h_bytes(int64_t M, int64_t R) {
 
 size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R) {
   if (M < 0 || R <= 0) return 0;
-  return static_cast<size_t>(3 * round_up(4 * M * R, 256) + 4 * R * 2 * LORA_WG_COLS * LORA_WG_MAX_CTAS);   // dH, its parts, H's parts, partial sums
+  return static_cast<size_t>(round_up(4 * M * R, 256) + 2 * round_up(6 * M * R, 256) + 4 * R * 2 * LORA_WG_COLS * LORA_WG_MAX_CTAS);   // dH, its parts, H's parts, partial sums
 }
 
 qlin_status qlin_lora_backward(const void* dY, const void* X, qlin_dtype xdt, int64_t M, int64_t K, const void* A, const void* B,
@@ -1821,12 +1821,12 @@ qlin_status qlin_lora_backward(const void* dY, const void* X, qlin_dtype xdt, in
   DeviceInfo* d;
   QLIN_TRY(device_info(&d));
   const LoraCall c{M, L, R, static_cast<const int*>(plan), scale, d, st};
-  const int64_t rows_bytes = round_up(4 * M * R, 256);
+  const int64_t rows_bytes = round_up(4 * M * R, 256), parts_bytes = round_up(6 * M * R, 256);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* dH = reinterpret_cast<float*>(ws);
   uint16_t* dHs = reinterpret_cast<uint16_t*>(ws + rows_bytes);
-  uint16_t* Hs = reinterpret_cast<uint16_t*>(ws + 2 * rows_bytes);
-  float* part = reinterpret_cast<float*>(ws + 3 * rows_bytes);
+  uint16_t* Hs = reinterpret_cast<uint16_t*>(ws + rows_bytes + parts_bytes);
+  float* part = reinterpret_cast<float*>(ws + rows_bytes + 2 * parts_bytes);
   using T = __nv_bfloat16;
   QLIN_TRY((launch_lora_shrink<T, true>(c, dY, N, B, scale, dH, LoraSplit{dHs, H, Hs})));
   QLIN_TRY(R <= 64 ? launch_lora_wgrad<1>(c, X, K, dHs, dA, dY, N, Hs, dB, part) : launch_lora_wgrad<2>(c, X, K, dHs, dA, dY, N, Hs, dB, part));

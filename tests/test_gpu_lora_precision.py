@@ -121,3 +121,52 @@ def test_gradient_is_summed_in_short_chains(q):
     want = torch.cat([dY[:, n:n + 1024].double().T @ H.double() for n in range(0, N, 1024)]).to(dtype)
     e = 2 * (64 + 1) / 2 * 2.0 ** -23 + 8 * 2.0 ** -25
     assert (dB[0] != want).float().mean().item() <= 2.0 ** 8 * e
+
+
+def _two_rows(M, L):
+    """For each adapter of idx = m % L: a row among the first and one among the last, of other tiles or MMAs."""
+    return [(a, a + (M - L) // L * L) for a in range(L)]
+
+
+@pytest.mark.parametrize("R", [8, 72])
+def test_db_sees_all_bits_of_h(q, R):
+    # rows +c and -c of dY against rows of H that differ by 2^-12: what is left of the sum shows how exactly H entered.
+    # Two MMAs with anything in them lose four steps each, the parts are added in two roundings.
+    dtype, M, K, N, L = torch.bfloat16, 300, 32, 520, 3
+    g = torch.Generator(device="cuda").manual_seed(R)
+    idx = (torch.arange(M, device="cuda") % L).to(torch.int32)
+    H = 0.5 + torch.rand((M, R), generator=g, device="cuda")
+    dY, c = torch.zeros((M, N), dtype=dtype, device="cuda"), _positive(g, (N,), dtype)
+    scale = 0.5 + torch.rand(L, generator=g, device="cuda")
+    want, size = torch.zeros((L, N, R), dtype=torch.float64, device="cuda"), torch.zeros((L, N, R), dtype=torch.float64, device="cuda")
+    for a, (i, j) in enumerate(_two_rows(M, L)):
+        H[j] = H[i] * (1 + 2.0 ** -12 * torch.rand(R, generator=g, device="cuda"))
+        dY[i], dY[j] = c, -c
+        want[a] = scale[a].double() * torch.outer(c.double(), H[i].double() - H[j].double())
+        size[a] = scale[a].double() * torch.outer(c.double(), H[j].double())
+    X, A, B = _positive(g, (M, K), dtype), _positive(g, (L, R, K), dtype), _positive(g, (L, N, R), dtype)
+    _, _, dB = q.qlin_lora_backward(dY, X, A, B, scale, q.qlin_lora_plan(idx, L), H)
+    e = (4 + 4 + 1) * 2.0 ** -23 * size
+    assert ((dB.double() - want).abs() <= e + 2.0 ** -8 * (want.abs() + e)).all()
+
+
+@pytest.mark.parametrize("R", [8, 72])
+def test_da_sees_all_bits_of_dh(q, R):
+    # the same for dA: rows +x and -x of X against dH = s (d1 B[n1] + d2 B[n2]) whose d2, 2^-12 of d1, differ. The MMA
+    # and the scale of each dH lose four steps and half a one.
+    dtype, M, K, N, L = torch.bfloat16, 300, 528, 16, 3
+    g = torch.Generator(device="cuda").manual_seed(R)
+    idx = (torch.arange(M, device="cuda") % L).to(torch.int32)
+    A, B = _positive(g, (L, R, K), dtype), _positive(g, (L, N, R), dtype)
+    dY, X, x = torch.zeros((M, N), dtype=dtype, device="cuda"), torch.zeros((M, K), dtype=dtype, device="cuda"), _positive(g, (K,), dtype)
+    scale = 0.5 + torch.rand(L, generator=g, device="cuda")
+    want, size = torch.zeros((L, R, K), dtype=torch.float64, device="cuda"), torch.zeros((L, R, K), dtype=torch.float64, device="cuda")
+    for a, (i, j) in enumerate(_two_rows(M, L)):
+        dY[i, 3] = dY[j, 3] = 1.5
+        dY[i, 11], dY[j, 11] = 2.0 ** -12, 2.0 ** -13
+        X[i], X[j] = x, -x
+        dh = scale[a].double() * (dY[[i, j]].double() @ B[a].double())
+        want[a], size[a] = torch.outer(dh[0] - dh[1], x.double()), torch.outer(dh[0], x.double())
+    _, dA, _ = q.qlin_lora_backward(dY, X, A, B, scale, q.qlin_lora_plan(idx, L), torch.zeros((M, R), device="cuda"))
+    e = (2 * (4 + 0.5) + 4 + 4 + 1) * 2.0 ** -23 * size
+    assert ((dA.double() - want).abs() <= e + 2.0 ** -8 * (want.abs() + e)).all()
