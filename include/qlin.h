@@ -294,7 +294,9 @@ QLIN_API qlin_status qlin_layer_norm_fp8_prep(const void *X, qlin_dtype xdt, int
                                      float *s_x, void *stream);
 
 /* The same for qlin_w4a8_gemm: per-token int8 codes (round half to even) and
- * s_x[i] = max_k |y| / 127. */
+ * s_x[i] = max_k |y| / 127. A row with a NaN among its y (of a NaN or infinite
+ * X, all of them are) has s_x = NaN, here and in the dynamic FP8 form, so that
+ * the GEMM's row is NaN too; its int8 codes are 0. */
 QLIN_API qlin_status qlin_layer_norm_w4a8_prep(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *gamma,
                                       const void *beta, float eps, int8_t *Xq, float *s_x, void *stream);
 

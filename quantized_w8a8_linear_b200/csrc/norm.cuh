@@ -37,23 +37,25 @@ struct NormArgs {
   const float* x_scale;    // [1] static scale
 };
 
-// Sum (or maximum) over the CTA, the same value in every thread and in a
-// fixed order. Consecutive calls alternate between two rows of `red`, so one
+// Sum (or maximum of absolute values) over the CTA, the same value in every
+// thread and in a fixed order. The maximum is taken of the bit patterns, which
+// order like the values and put a NaN above them all: fmaxf would drop it, and
+// a row of NaN leave as zeros with a scale of zero. Consecutive calls alternate between two rows of `red`, so one
 // barrier a call is enough: a row is written again only after every thread
 // has passed the next call's barrier, behind its reads of this one.
 template <bool MAX>
 __device__ __forceinline__ float cta_reduce(float v, float (*red)[16], int& slot) {
-  v = MAX ? warp_max(v) : warp_sum(v);
+  v = MAX ? __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))) : warp_sum(v);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return v;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) red[slot][warp] = v;
   __syncthreads();
-  float t = (lane & 15) < warps ? red[slot][lane & 15] : (MAX ? -INFINITY : 0.0f);
+  float t = (lane & 15) < warps ? red[slot][lane & 15] : 0.0f;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     const float u = __shfl_xor_sync(0xffffffffu, t, o);
-    t = MAX ? fmaxf(t, u) : t + u;
+    t = MAX ? __uint_as_float(max(__float_as_uint(t), __float_as_uint(u))) : t + u;
   }
   slot ^= 1;
   return t;
@@ -177,15 +179,15 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_fwd(const NormArgs a)
     } else {
       float inv = inv_static;
       if constexpr (OUT != NORM_OUT_E4M3_STATIC) {
-        float m = 0.0f;
+        uint32_t m = 0;   // the largest |y|, as bits
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           if (j * nt + tid < KV) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(lo_f(x[j][i])), fabsf(hi_f(x[j][i]))));
+            for (int i = 0; i < 4; ++i) m = max(m, max(__float_as_uint(fabsf(lo_f(x[j][i]))), __float_as_uint(fabsf(hi_f(x[j][i])))));
           }
         }
-        const float sx = cta_reduce<true>(m, red, slot) / (OUT == NORM_OUT_INT8 ? 127.0f : 448.0f);
+        const float sx = cta_reduce<true>(__uint_as_float(m), red, slot) / (OUT == NORM_OUT_INT8 ? 127.0f : 448.0f);
         inv = 1.0f / sx;
         if (tid == 0) a.s_x[row] = sx;
       }
