@@ -485,11 +485,9 @@ struct LoraShrinkParams {
   uint16_t* Gs;         // [M,3,R]
 };
 
-// RB: ceil(R / 64). DEEP: one CTA an SM with four stages, for tiles enough to
-// fill the SMs without clusters (16640 x 4096 rows at rank 64: 30 us against
-// 36 with two CTAs of two stages each); else two CTAs an SM, in clusters (64
-// tiles of 12288: 47 us in clusters of four, 52 with one deep CTA in clusters
-// of two). Above rank 64 a stage is larger: three of them, one CTA.
+// RB: ceil(R / 64). DEEP: one CTA an SM with four stages, where the tiles would
+// not give each SM two of two stages; launch_lora_shrink has the rule and both
+// sides' times. Above rank 64 a stage is larger: three of them, one CTA.
 // ACCS accumulators take the stages in turn, as many as the CTAs of an SM have
 // TMEM for: an MMA cuts its fp32 sum off instead of rounding it, so a sum of
 // 4096 products in one chain of 256 MMAs came out 4e-6 of its size too small

@@ -1648,11 +1648,19 @@ qlin_status launch_lora_shrink_rb(const LoraCall& c, const void* X, int64_t C, c
   constexpr int smem = LoraShrinkSmem<RB, DEEP>::TOTAL;
   static std::atomic<bool> set[16] = {};
   QLIN_TRY(allow_smem(kern, smem, set));
-  // the largest cluster whose CTAs are resident together, and that leaves every
-  // CTA a block of the contraction
-  const int64_t slots = (RB == 2 || DEEP ? 1 : 2) * c.d->sms;
-  int cluster = 8;
-  while (cluster > 1 && (tiles * cluster > slots || cluster > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) cluster /= 2;
+  // The largest cluster that leaves every CTA a block of the contraction and of
+  // which the tiles' are resident together. A cluster lies within a GPC, so on
+  // 148 SMs fewer fit than there are slots, as measured: 33 of eight and 71 of
+  // four with two CTAs an SM, 15 and 33 with one. Past that the last ones run
+  // behind the others: 36 tiles of 4096 columns, rank 16, take 19.4 us in
+  // clusters of eight, 15.5 in clusters of four; 74 tiles 23.5 in clusters of
+  // four, 20.3 in clusters of two. (cudaOccupancyMaxActiveClusters counts as if
+  // one CTA fitted an SM.)
+  constexpr bool ONE = RB == 2 || DEEP;
+  const int64_t fits[4] = {(ONE ? 148 : 296), (ONE ? 74 : 148), (ONE ? 33 : 71), (ONE ? 15 : 33)};
+  int log2 = 3;
+  while (log2 > 0 && (tiles > fits[log2] * c.d->sms / 148 || (1 << log2) > (C + LORA_SHRINK_BK - 1) / LORA_SHRINK_BK)) --log2;
+  const int cluster = 1 << log2;
   LoraShrinkParams p{c.view(), C, static_cast<int>(c.R), static_cast<const uint16_t*>(X), scale, H, sp.Hs, sp.G, sp.Gs};
   return launch_dependent(kern, "k_lora_shrink launch", dim3(static_cast<unsigned>(lora_max_tiles(c.M, c.L) * cluster)), LORA_SHRINK_THREADS, smem, cluster, c.st, tw, p, cluster);
 }
@@ -1660,7 +1668,14 @@ template <typename T, bool W_MN>
 qlin_status launch_lora_shrink(const LoraCall& c, const void* X, int64_t C, const void* W, const float* scale, float* H, const LoraSplit& sp = {}) {
   const int64_t tiles = c.tiles();
   if (c.R > 64) return launch_lora_shrink_rb<T, 2, W_MN, false>(c, X, C, W, scale, H, sp, tiles);
-  if (2 * tiles > c.d->sms) return launch_lora_shrink_rb<T, 1, W_MN, true>(c, X, C, W, scale, H, sp, tiles);
+  // One CTA an SM with twice the stages, or two (or clusters of them): one, where
+  // the last tiles would take most SMs but not two CTAs each; behind other tiles,
+  // from a quarter of the SMs on. X of 4096 columns, us, one CTA against two:
+  //   rank 64: tiles 76 26.9, 24.6   90 28.1, 28.8   130 34.2, 36.5   150 58, 47   260 66, 63   400 94, 100
+  //   rank 16: tiles 76 25.7, 20.7   90 26.5, 22.7   130 34.4, 34.0   150 56, 44   260 62, 58   400 90, 92
+  // and of 12288, rank 64: 130 76, 78   150 134, 109   260 146, 142   300 208, 221   400 217, 247
+  const int64_t sms = c.d->sms, last = tiles % (2 * sms);
+  if (last <= sms && 4 * last > (tiles > 2 * sms ? 1 : 3) * sms) return launch_lora_shrink_rb<T, 1, W_MN, true>(c, X, C, W, scale, H, sp, tiles);
   return launch_lora_shrink_rb<T, 1, W_MN, false>(c, X, C, W, scale, H, sp, tiles);
 }
 
