@@ -596,11 +596,13 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
     }
     cp_async_commit();
     cp_async_wait<0>();
-    if (threadIdx.x == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);
     // ---------------- epilogue: row q * 32 + lane of the tile ----------------
     const int q = warp;
     const int r = q * 32 + lane;
-    good = good && mbar_wait_warp(tfull_bar, 0, abort_flag) && kb1 > kb0;
+    good = good && mbar_wait_warp(tfull_bar, 0, abort_flag);
+    if (!good && threadIdx.x == 0) drain_ring(full_bar, S::STAGES, stage, phase, issued);   // else the MMAs have read them all
+    __syncwarp();
+    good = good && kb1 > kb0;
     tc_fence_after();
     const float s = p.scale != nullptr ? __ldg(p.scale + a) : 1.0f;
     float* out = cluster > 1 ? reinterpret_cast<float*>(smem) + r * (Rp + 4) : p.H + static_cast<int64_t>(r < n ? rows[r] : 0) * p.R;
@@ -750,7 +752,8 @@ struct LoraExpandSmem {
   static constexpr int Y_ROW = 272;
   static constexpr int Y_BYTES = LORA_TILE * Y_ROW;
   static constexpr int BAR_BYTES = 8 * (2 * V_STAGES + 2 * Y_STAGES + 7) + 16;
-  static constexpr int TOTAL = 1024 + 3 * H_BYTES + V_STAGES * V_BYTES + Y_STAGES * Y_BYTES + BAR_BYTES;
+  static constexpr int UP_BYTES = 2 * LORA_TILE * 4;                   // fp16: powers of two of the rows
+  static constexpr int TOTAL = 1024 + 3 * H_BYTES + V_STAGES * V_BYTES + Y_STAGES * Y_BYTES + UP_BYTES + BAR_BYTES;
   static_assert(TOTAL <= 227 * 1024, "k_lora_expand shared memory");
 };
 
@@ -762,7 +765,8 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
   uint8_t* sH = smem;   // [3 parts][RB][128 rows][128 bytes]
   auto sV = [&](int s) { return smem + 3 * S::H_BYTES + s * S::V_BYTES; };
   auto sY = [&](int s) { return smem + 3 * S::H_BYTES + S::V_STAGES * S::V_BYTES + s * S::Y_BYTES; };
-  uint64_t* vfull_bar = reinterpret_cast<uint64_t*>(smem + 3 * S::H_BYTES + S::V_STAGES * S::V_BYTES + S::Y_STAGES * S::Y_BYTES);
+  float* sUp = reinterpret_cast<float*>(smem + 3 * S::H_BYTES + S::V_STAGES * S::V_BYTES + S::Y_STAGES * S::Y_BYTES);   // [2][128]
+  uint64_t* vfull_bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sUp) + S::UP_BYTES);
   uint64_t* vempty_bar = vfull_bar + S::V_STAGES;
   uint64_t* yfull_bar = vempty_bar + S::V_STAGES;
   uint64_t* yempty_bar = yfull_bar + S::Y_STAGES;
@@ -941,6 +945,7 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
     int stage = 0, n = 0, my_row = 0;
     float s = 1.0f;    // scale[a], times the power of two of the lane's row (fp16)
     uint32_t phase = 0, acc_phase = 0, h_phase = 0;
+    int up_at = 0;     // half of sUp: tiles alternate, since a warp may be splitting the next one while another has not read this one's
     bool next = true, good = true;
     for (int64_t u = u0, t = t0, nb = nb0; u < u1; ++u) {
       if (next) {
@@ -955,19 +960,15 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
           if (!good) break;
           h_phase ^= 1u;
         }
-        const float sa = p.scale != nullptr ? __ldg(p.scale + info.x) : 1.0f;
-        s = sa;
+        s = p.scale != nullptr ? __ldg(p.scale + info.x) : 1.0f;
         constexpr bool F16 = std::is_same<T, __half>::value;
         constexpr int CH = RB * 8;   // 8-value chunks of a row: lanes of a warp that share a row
-        // the four warps of these rows take every fourth step of 32 / CH rows; in
-        // fp16 all look at all of them, for their lanes' powers of two
+        // the four warps of these rows take every fourth step of 32 / CH rows
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const bool mine = (i & 3) == 2 * group + half;
-          if (!F16 && !mine) continue;
-          const int e = i * 32 + lane, r = e / CH, c = e % CH;
+        for (int i0 = 0; i0 < CH; i0 += 4) {
+          const int e = (i0 + 2 * group + half) * 32 + lane, r = e / CH, c = e % CH;
+          const int row = __shfl_sync(0xffffffffu, my_row, r), rr = q * 32 + r;
           float f[8] = {};
-          const int row = __shfl_sync(0xffffffffu, my_row, r);
           if (r < n && 8 * c < p.R) {
             const float4* src = reinterpret_cast<const float4*>(p.H + static_cast<int64_t>(row) * p.R + 8 * c);
             const float4 x = src[0], y = src[1];
@@ -982,26 +983,26 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
             for (int o = CH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             // up = 2^(e - 14) with 2^e <= max < 2^(e+1), down = 1 / up; rows with infinities or NaN keep 1
             const uint32_t em = __float_as_uint(m) >> 23, eb = em > 15u ? em - 14u : 1u;
-            const float up = em < 255u ? __uint_as_float(eb << 23) : 1.0f;
             const float down = em < 255u ? __uint_as_float((254u - eb) << 23) : 1.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= down;
-            // the lane whose TMEM row this is keeps 2^e: rows of this step are r of lanes 0, CH, ...
-            const float up_mine = __shfl_sync(0xffffffffu, up, (lane % (32 / CH)) * CH);
-            if (lane / (32 / CH) == i) s = sa * up_mine;
+            if (c == 0) sUp[up_at * LORA_TILE + rr] = em < 255u ? __uint_as_float(eb << 23) : 1.0f;
           }
-          if (mine) {
-            uint4 part[3];
-            split8<T>(f, part);
-            const int rr = q * 32 + r;
-            uint8_t* h = sH + (c >> 3) * (LORA_TILE * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+          uint4 part[3];
+          split8<T>(f, part);
+          uint8_t* h = sH + (c >> 3) * (LORA_TILE * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
 #pragma unroll
-            for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(h + j * S::H_BYTES) = part[j];
-          }
+          for (int j = 0; j < 3; ++j) *reinterpret_cast<uint4*>(h + j * S::H_BYTES) = part[j];
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(hfull_bar);
+        if constexpr (F16) {   // the power of two of the lane's own row, from the warp that split it
+          good = mbar_wait_warp(hfull_bar, static_cast<uint32_t>(up_at), abort_flag);
+          if (!good) break;
+          s *= sUp[up_at * LORA_TILE + q * 32 + lane];
+          up_at ^= 1;
+        }
       }
       if (((u - u0) & 1) == group) {
       good = mbar_wait_warp(&tfull_bar[group], acc_phase, abort_flag) && mbar_wait_warp(&yfull_bar[stage], phase, abort_flag);
