@@ -325,7 +325,8 @@ QLIN_API size_t qlin_lora_plan_bytes(int64_t M, int64_t L);
  * qlin_lora_plan_bytes(M, L) bytes, opaque, read by the calls below with the
  * same M and L (a buffer that holds another M or L leaves their outputs
  * unwritten, dA and dB zero, and QLIN_ERR_INVALID_ARG in the device status
- * word). 1 <= L <= 1024, M <= 2^28. */
+ * word; a plan of another batch of the same M and L is not noticed and applies
+ * that batch's adapters). 1 <= L <= 1024, M <= 2^28. */
 QLIN_API qlin_status qlin_lora_plan(const int32_t *idx, int64_t M, int64_t L, void *plan, size_t plan_bytes,
                            void *stream);
 
@@ -339,11 +340,16 @@ QLIN_API size_t qlin_lora_forward_h_bytes(int64_t M, int64_t R);
  * A [L,R,K] and B [L,N,R] in xdt, scale fp32 [L], all R alike (shorter
  * adapters are padded with zeros). Rows without an adapter keep their Y, bit
  * for bit. H [M,R] fp32 is written for rows that have one: kept for the
- * backward pass, else scratch, or NULL where qlin_lora_forward_h_bytes is 0. H enters the second product as two 16-bit
- * parts (16 significant bits in bf16, 22 in fp16); all sums are fp32 and Y is
- * rounded once. R % 8 == 0, 8 <= R <= 128; N is arbitrary up to 2^28. A row's result does
- * not depend on the other rows of the batch beyond the order in which its K
- * products are added. Y and H overlap no other argument. */
+ * backward pass, else scratch, or NULL where qlin_lora_forward_h_bytes is 0.
+ * All sums are fp32, H enters the second product with fp32's 24 bits, and Y is
+ * rounded once: few rows (where qlin_lora_forward_h_bytes is 0) by fp32 FMAs,
+ * more on the tensor cores with H in three 16-bit parts (in fp16 all 24 bits of
+ * what is above 2^-15 of a row's largest |H|, of the rest what is above 2^-39 of
+ * it). A row's result depends on the other rows of the batch only through the
+ * order of its sums over K and R. A row of X with NaN or infinities makes its
+ * own Y so, and an infinite or NaN weight those of its adapter's rows that it
+ * reaches (as NaN, where parts of H are 0). R % 8 == 0, 8 <= R <= 128; N is
+ * arbitrary up to 2^28. Y and H overlap no other argument. */
 QLIN_API qlin_status qlin_lora_forward(const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A, const void *B,
                               const float *scale, int64_t L, int64_t R, int64_t N, const void *plan,
                               size_t plan_bytes, float *H, void *Y, void *stream);
@@ -358,9 +364,9 @@ QLIN_API size_t qlin_lora_backward_workspace_bytes(int64_t M, int64_t R);
  *   dA[a] = xdt(sum_i dH[i]^T X[i]),  dB[a] = xdt(scale[a] * sum_i dY[i]^T H[i])
  *           over the adapter's rows; zeros for an adapter without rows.
  * dA and dB are written, not added to, in an order of sums that does not
- * depend on timing. xdt must be QLIN_BF16 (the parts of dH need fp32's
- * exponent range); N % 8 == 0. M = 0 writes zeros to dA and dB. Outputs
- * overlap no other argument. */
+ * depend on timing; sums are fp32, and H and dH enter them with 24 bits. xdt
+ * must be QLIN_BF16 (the parts of dH need fp32's exponent range); N % 8 == 0.
+ * M = 0 writes zeros to dA and dB. Outputs overlap no other argument. */
 QLIN_API qlin_status qlin_lora_backward(const void *dY, const void *X, qlin_dtype xdt, int64_t M, int64_t K, const void *A,
                                const void *B, const float *scale, int64_t L, int64_t R, int64_t N,
                                const void *plan, size_t plan_bytes, const float *H, void *dX, void *dA,
@@ -459,8 +465,9 @@ QLIN_API qlin_status qlin_int8_outlier_forward_noalloc(const void *X, qlin_dtype
 /* ---------------- status ------------------------------------------------------------ */
 
 /* Reads (and with reset != 0 clears) the device status word of the current
- * device into *status (host pointer): QLIN_OK, or QLIN_ERR_TIMEOUT if a
- * kernel gave up on a bounded wait. Synchronises the device. */
+ * device into *status (host pointer): QLIN_OK, QLIN_ERR_TIMEOUT if a kernel
+ * gave up on a bounded wait, or QLIN_ERR_INVALID_ARG if an adapter call was
+ * given a plan of another M or L. Synchronises the device. */
 QLIN_API qlin_status qlin_get_device_status(int32_t *status, int reset);
 
 /* Sets the limit of every bounded device-side wait, in nanoseconds (default

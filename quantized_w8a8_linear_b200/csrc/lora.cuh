@@ -27,8 +27,8 @@
 // bits, so that a row comes out the same as where H stays fp32 (k_lora_rows).
 // With two parts, 16 bits in bf16, 2^-17 of the update showed in Y where it
 // cancels, and more of Y's elements than an fp32 product has rounded the other
-// way; the third one costs the forward pass 1 to 5% (16640 x 4096 -> 12288,
-// rank 64: 198 us in all, 190 with two) and the backward pass 2 to 6%, 17% above
+// way; the third one costs the forward pass up to 4% (16640 x 4096 -> 12288,
+// rank 64: 197 us in all, 189 with two) and the backward pass 2 to 8%, 17% above
 // rank 64. The smallest go first, while the accumulator is small. fp16
 // parts are taken of h 2^14 / 2^e with 2^e the largest power of two in the row
 // (exact): nothing overflows, all 24 bits of what is above 2^-15 of the row's
@@ -313,8 +313,9 @@ __device__ __forceinline__ void store_split4(uint16_t* row, int R, const float4&
 // move 20 MB, 3 us of HBM time): the CTAs ask for their part of B and Y into
 // L2 before they turn to A, and there is no second launch. fp32 FMAs: at these
 // sizes the tensor cores would wait for the same bytes. One row 4096 -> 4096
-// at rank 16 takes 6 us in a graph of such calls (10 through the two kernels
-// below), 64 rows of 32 adapters 7 (19).
+// at rank 16 takes 5 us in a graph of such calls (10 through the two kernels
+// below), 64 rows of 32 adapters 7 (21): with A, B and Y in L2. With cold caches
+// they take 8 us, and 64 rows of 32 adapters 4096 -> 12288 15 (10 warm).
 // ---------------------------------------------------------------------------
 constexpr int LORA_ROWS_THREADS = 256, LORA_ROWS_CLUSTER = 8;
 
@@ -543,7 +544,9 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  // X, the plan and H's earlier readers belong to kernels before this one
+  // X, the plan and H's earlier readers belong to kernels before this one. In
+  // this order: k_lora_expand starts on the release and reads the plan and Y
+  // before its own wait, so all that wrote them must have ended by now
   griddep_wait();
   griddep_launch_dependents();
 
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(LORA_SHRINK_THREADS)
 // stores took longer than a unit's bytes. 256 bytes of a row at a
 // time are what HBM wants: reading and writing 128 rows of 24 KB in place,
 // walked in pieces of 64, 128, 256 and 512 bytes, runs at 4.2, 4.6, 5.2 and
-// 5.3 TB/s; 16640 rows of 12288 at rank 64 take 155 us, 5.3 TB/s. The copies
+// 5.3 TB/s; 16640 rows of 12288 at rank 64 take 151 us, 5.4 TB/s. The copies
 // of Y and V start before the kernel that makes H has ended (programmatic
 // dependent launch); only the readers of H wait for it.
 //   VEC false: rows of Y that are not multiples of 16 bytes. A row's piece
@@ -809,6 +812,9 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  // The plan, Y and V are read from here on, H only behind griddep_wait: the
+  // kernel before this one is k_lora_shrink, k_lora_wgrad or its join, and none
+  // of them lets this one start before all earlier kernels have ended
   const int nbs = static_cast<int>((p.N + LORA_EXPAND_BN - 1) / LORA_EXPAND_BN);
   const int64_t units = static_cast<int64_t>(p.plan.tiles()) * nbs;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
@@ -1147,14 +1153,15 @@ __global__ void __launch_bounds__(LORA_EXPAND_THREADS, 1) k_lora_expand(const __
 // memory (one 128-byte row per step of the contraction), so nothing is
 // transposed. Sums stay in TMEM over the tiles of an adapter: an MMA cuts its
 // accumulator off instead of rounding it, so every LORA_WG_CHAIN tiles the
-// epilogue adds it, rounded, to sums of its own beside it (one chain over 8192
-// positive rows came out 5e-5 too small, chains of 1024 rows 6e-6). The
-// accumulators of a unit's two MMAs are handed back one by one, and the copies
-// run on meanwhile, so it costs no time. An adapter whose
+// epilogue adds it, rounded, to sums of its own beside it (of the bf16 sums over
+// 8192 rows of positive products one chain put 0.28% on the wrong side of a
+// rounding, chains of 1024 rows 0.012%). The accumulators of a unit's two MMAs
+// are handed back one by one, and the copies run on meanwhile: 154 us for a
+// backward pass that took 157 with two accumulators in turn. An adapter whose
 // tiles are cut between CTAs leaves fp32 partial sums, slot 0 for a CTA's
 // first segment if it began before, slot 1 for the last one, and
 // k_lora_wgrad_join adds them in CTA order. 8191 rows, 4096 and 12288 columns,
-// rank 64: 59 us, 4.5 TB/s of X and dY (the join 9).
+// rank 64: 70 us, 3.8 TB/s of X and dY (the join 9).
 // bf16 only: G's parts need fp32's exponent range (a power of two per row, as
 // k_lora_expand takes out, does not leave a sum over rows).
 // ---------------------------------------------------------------------------
@@ -1257,7 +1264,7 @@ __global__ void __launch_bounds__(LORA_WG_THREADS, 1) k_lora_wgrad(const LoraWgr
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();   // dH, and the partial slots' earlier readers
-  griddep_launch_dependents();
+  griddep_launch_dependents();   // in this order: k_lora_expand reads the plan and dX before its own wait
 
   const LoraWgradUnits un(p);
   const int64_t u0 = un.first(blockIdx.x), u1 = un.first(blockIdx.x + 1);

@@ -549,8 +549,14 @@ qlin_status int8_outlier_gemm_ws(qlin_dtype xdt, int64_t M, int64_t K, const int
   return launch_gemm<0, EPI_INT8_OUTLIER, __half>(w.Xq, Wq, ep, st, 2, w.sk_ctas);
 }
 
-// CTAs of k_norm_bwd at most: each leaves 2 K fp32 column sums for the second
-// kernel, so wide rows take two CTAs per SM, narrower ones four.
+// CTAs of k_norm_bwd at most, in whole multiples of a B200's 148 SMs (workspace
+// sizes are asked without a device). Each leaves 2 K fp32 column sums for the
+// second kernel. Rows of 1025 to 2560 columns, one a CTA at a time, leave room for
+// three or four CTAs an SM, which many rows need; us, 296 CTAs against 592:
+//   16640 rows: K 1040 49.1, 34.9   2048 56.2, 44.5   2560 61.2, 53.4   3088 68.9, 68.9
+//   2048 rows:  K 1040 11.0, 12.5   2048 11.9, 14.0   2560 13.2, 14.4   3088 15.2, 15.2
+// Above, no more than two fit (from 3088 columns on the two are the same), and
+// rows up to 1024 take a warp each, eight a CTA (K 1024, 16640 rows: 28.8, 28.8).
 int64_t norm_bwd_ctas(int64_t K) { return K > 1024 && K < 3500 ? 592 : 296; }
 
 #define QLIN_TRY(...)                  \
@@ -1431,7 +1437,8 @@ qlin_status launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
   if (s != QLIN_OK) return s;
   const int64_t KV = a.K / 8;
   // four vectors of a row a thread: 16640 rows of 4096 took 41 us with four, 52
-  // with two, 44 with eight, and 64 rows as long with four as with one (2.5 us).
+  // with two, 44 with eight (a graph of calls on the same rows, some of which
+  // stay in L2), and 64 rows as long with four as with one (2.6 us).
   // Over 8192 more, so that two rows still share an SM: 4352 rows of 12288 took
   // 39 us with six (256 threads), 44 with four (384, one row an SM).
   const int64_t most = KV <= 1024 ? 4 : KV <= 1536 ? 6 : KV <= 2048 ? 8 : KV <= 3072 ? 6 : 8;
@@ -1599,10 +1606,18 @@ namespace {
 constexpr int64_t kLoraMaxM = int64_t{1} << 28, kLoraMaxN = int64_t{1} << 28;
 constexpr int LORA_WG_MAX_CTAS = 160;
 
-// Which kernels take the forward pass. Measured at K = N = 4096, bf16, one
-// adapter and 32, us, k_lora_rows against the two tile kernels:
-//   R 16: M 64 7.0, 7.3 : 11.0, 18.9   M 256 8.4, 13.8 : 11.7, 20.4
-//   R 64: M 16 15.5, 12.5 : 10.6, 15.9   M 64 15.6, 18.0 : 11.4, 19.3
+// Which kernels take the forward pass. It goes by M and R alone, since a caller
+// asks by them whether H is needed (qlin_lora_forward_h_bytes). us, bf16,
+// k_lora_rows against the two tile kernels, one adapter and, behind the bar, 32:
+//   4096 -> 4096   R 16: M 64 6.9, 11.5 | 7.0, 21.2    M 256 8.2, 12.1 | 13.4, 21.9
+//                  R 32: M 64 9.6, 11.7 | 10.2, 21.6   M 256 12.1, 12.5 | 20.2, 22.1
+//                  R 64: M 16 15.3, 11.6               M 64 15.6, 12.3 | 17.3, 22.2
+//   4096 -> 12288  R 16: M 64 10.2, 11.4 | 10.4, 32.3  M 256 12.9, 15.1 | 21.4, 33.7
+//                  R 32: M 64 15.3, 11.8 | 16.1, 32.7  R 64: M 64 26.8, 12.5 | 31.2, 34.4
+//   12288 -> 4096  R 16: M 64 8.7, 15.4 | 8.6, 25.5    R 32: M 64 13.3, 15.9 | 14.6, 25.9
+//   1024 -> 1024   R 16: M 64 6.0, 9.9 | 5.9, 15.6     R 32: M 64 8.2, 10.2 | 8.5, 15.7
+// The tiles win where few adapters of rank 32 meet wide outputs (up to 4 us), the
+// rows everywhere else (up to 22 us).
 bool lora_by_rows(int64_t M, int64_t R) { return M <= LORA_OCTET_M && R <= 32 && M * R <= 4096; }
 
 // Adapter weights 16-bit [L, rows, cols]: box 64 columns x box_rows of one
