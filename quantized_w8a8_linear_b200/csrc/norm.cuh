@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(MAXT, 512 / MAXT) k_norm_bwd(const NormBwdArgs
   if constexpr (COLS) {
     float* p = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.K;
     float* mine = p;
-    if (groups > 1) {   // the ring's memory, when every warp is done with it: [groups][2][K] fp32, 8 K bytes a warp; a warp's share of the ring, 6 V vectors a lane, is 3072 V bytes, and K <= 256 V
+    if (groups > 1) {   // the ring's memory, when every warp is done with it: [groups][2][K] fp32, 8 K bytes a warp; a warp's share of the ring, 6 V vectors a lane, is 3 V KB, and K <= 256 V
       __syncthreads();
       mine = reinterpret_cast<float*>(norm_ring) + static_cast<int64_t>(group) * 2 * a.K;
     }
